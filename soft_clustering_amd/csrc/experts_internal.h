@@ -1,0 +1,92 @@
+// Shared by the kernels behind include/gmm_experts.h: storage types, 16-byte
+// pieces of a row, the map from workgroups to lists.
+#pragma once
+
+#include "common.h"
+#include "gmm_experts.h"
+
+namespace gmm {
+
+constexpr int64_t kMaxWidth = 1 << 20, kMaxStride = 1 << 22;
+constexpr int64_t kMaxEntries = 1 << 30;   // entries and slots are 32-bit, grids of them stay in range
+
+// fp32 -> storage type, round to nearest even.
+__device__ __forceinline__ void from_f32(float v, float* o) { *o = v; }
+__device__ __forceinline__ void from_f32(float v, bf16_t* o) { o->bits = __builtin_bit_cast(uint16_t, (__bf16)v); }
+__device__ __forceinline__ void from_f32(float v, _Float16* o) { *o = (_Float16)v; }
+
+template <typename T> __device__ __forceinline__ uint4 pack16(const float* v) {
+    constexpr int E = Vec16<T>::kElems;
+    T t[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) from_f32(v[i], t + i);
+    return __builtin_bit_cast(uint4, t);
+}
+
+// Workgroup -> rows of one list.  Row block `t` of a launch is either block
+// (t - t0_k) of the list k with the largest t0_k = offsets[k] / BM + k not
+// above t (a list of c rows spans at most the ceil(c / BM) blocks up to
+// t0_{k+1}, so rows / BM + K blocks cover every list without any host
+// knowledge of the lengths), or, with by_slot, the block that starts at slot
+// t (only every BM-th slot of a list starts one; fewer workgroups where there are
+// fewer rows than lists).  One wave finds k in two steps of 64 candidates.
+// Every offset is clamped to [0, rows]: whatever the array holds, the slots
+// stay inside the row buffers.
+struct ListRows {
+    int k;        // list, -1: nothing to do
+    int s0, s1;   // slots [s0, s1)
+};
+
+__device__ __forceinline__ int clamped_offset(const int32_t* offsets, int k, int rows) {
+    return min(max(offsets[k], 0), rows);
+}
+
+__device__ __forceinline__ ListRows find_rows(const int32_t* __restrict__ offsets, int K, int rows, int t,
+                                              int bm, bool by_slot) {
+    const int lane = threadIdx.x & 63;
+    auto before = [&](int k) {   // does list k start at or before block t
+        if (k >= K) return false;
+        const int o = clamped_offset(offsets, k, rows);
+        return (by_slot ? o : o / bm + k) <= t;
+    };
+    int seg = 0;
+    if (K > 64) seg = max(__popcll(__ballot(before(lane * 64))) - 1, 0);
+    int k = seg * 64 + __popcll(__ballot(before(seg * 64 + lane))) - 1;
+    k = __builtin_amdgcn_readfirstlane(k);
+    ListRows r = {-1, 0, 0};
+    if (k < 0 || k >= K) return r;
+    const int a = clamped_offset(offsets, k, rows), b = clamped_offset(offsets, k + 1, rows);
+    int s0;
+    if (by_slot) {
+        if ((t - a) % bm != 0) return r;
+        s0 = t;
+    } else {
+        const int64_t first = a + (int64_t)(t - (a / bm + k)) * bm;
+        if (first >= b) return r;
+        s0 = (int)first;
+    }
+    if (s0 >= b) return r;
+    r.k = k;
+    r.s0 = __builtin_amdgcn_readfirstlane(s0);
+    r.s1 = __builtin_amdgcn_readfirstlane(b);
+    return r;
+}
+
+inline int64_t row_blocks(int64_t rows, int64_t k, int bm, bool* by_slot) {
+    const int64_t by_list = rows / bm + k;
+    *by_slot = rows < by_list;
+    return *by_slot ? rows : by_list;
+}
+
+inline bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
+inline int elem_size(int dtype) { return dtype == GMM_F32 ? 4 : 2; }
+
+// Argument checks shared by the calls on lists.
+gmm_status check_routes(const gmm_routes* r);
+gmm_status check_shape(int64_t n, int64_t m, int64_t k);
+gmm_status check_width(int64_t d, int32_t dtype);
+gmm_status check_stride(int64_t ld, int64_t d);
+
+inline gmm_status launched() { return hipGetLastError() == hipSuccess ? GMM_OK : GMM_E_HIP; }
+
+}  // namespace gmm

@@ -93,7 +93,11 @@ _lib = _load()
 EXPORTED = ("gmm_workspace_bytes", "gmm_prepare", "gmm_em_step", "gmm_finalize", "gmm_loglik",
             "gmm_assign", "gmm_fit", "gmm_get_stats", "gmm_diagnostics", "gmm_status_str", "gmm_version",
             "gmm_calib_sink_bytes", "gmm_calib_read", "gmm_calib_mfma", "gmm_calib_mfma_flops",
-            "gmm_em_iteration_noalloc", "gmm_noalloc_max_workspace")
+            "gmm_em_iteration_noalloc", "gmm_noalloc_max_workspace",
+            # the lists and the components' models (bound in experts.py)
+            "gmm_route_workspace_bytes", "gmm_route", "gmm_dispatch", "gmm_dispatch_backward", "gmm_combine",
+            "gmm_combine_backward", "gmm_linear", "gmm_linear_backward_workspace_bytes", "gmm_linear_backward",
+            "gmm_quantize4", "gmm_linear4")
 
 
 def status_str(status: int) -> str:

@@ -6,13 +6,17 @@
 //   dW_k  = sum_s dy[s] x_s^T   contraction over the list's rows; neither is contiguous along it
 //   db_k  = sum_s dy[s]
 //
-// A workgroup of four waves computes a 128 x 128 tile, each wave 64 x 64 as 2 x 2
-// blocks of v_mfma_f32_32x32x16 (16-bit storage) or v_mfma_f32_32x32x2_f32, fp32 accumulators.
-// Operand tiles go through LDS in 16-byte pieces, 128 bytes of the contraction (64 or 32 elements)
-// a step, two buffers.  An operand contiguous along the contraction is kept
-// [row][128 bytes], its pieces XOR-swizzled by the row, and read a fragment (8 or 4 elements) at a time; one that is
-// contiguous along the output is kept [contraction][128 columns] and read with
-// ds_read_b64_tr_b16 (16-bit) or element by element (fp32).
+// A workgroup computes a tile of 64 x 64 blocks, one a wave, each as 2 x 2 blocks of
+// v_mfma_f32_32x32x16 (16-bit storage) or v_mfma_f32_32x32x2_f32, fp32 accumulators.  Operand
+// tiles go through LDS in 16-byte pieces, 128 bytes of the contraction (64 or 32
+// elements) a step, two buffers: the pieces of step i + 1 are fetched while step i is
+// multiplied, straight into LDS (global_load_lds) where rows allow 16-byte pieces, through
+// registers where they do not.  An operand contiguous along the contraction is
+// kept [row][128 bytes], its pieces XOR-swizzled by the row, and read a fragment (8 or 4
+// elements) at a time; one that is contiguous along the output is kept
+// [contraction][columns] and read with ds_read_b64_tr_b16 (16-bit) or element by
+// element (fp32).  Pieces beyond a row's end, a list's end or the contraction come
+// from 16 zero bytes, so they add nothing.
 //
 // Workgroup -> rows: find_rows (experts_internal.h); the host never learns the lists' lengths.
 
@@ -29,8 +33,33 @@ typedef short short4v __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) short4v lds_short4;
 typedef __attribute__((address_space(3))) char lds_char;
 
-constexpr int kTile = 128;        // rows and columns of a workgroup's tile
-constexpr int kTileBytes = kTile * 128;   // one operand, one step
+// Waves of a workgroup along the rows and along the columns of its tile.
+template <int WM, int WN> struct Shape {
+    static constexpr int kThreads = 64 * WM * WN, kM = 64 * WM, kN = 64 * WN;
+    static constexpr int kABytes = kM * 128, kBBytes = kN * 128;   // one operand, one step
+    static constexpr int kWaves = WM * WN;
+};
+
+__device__ __constant__ uint4 zero_piece = {0, 0, 0, 0};
+
+// 16 bytes from each lane's address to LDS bytes lds + 16 lane, asynchronously: the wave that
+// issued it waits with wait_pieces() before the barrier that hands the tile over.  Written as asm
+// because the compiler, which tracks the builtin form as an LDS store, would wait
+// for the pieces of the next step before it reads those of this one.
+__device__ __forceinline__ void fetch_piece(const void* g, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(g) : "memory", "m0");
+}
+__device__ __forceinline__ void wait_pieces() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p);
+}
+
+// e / m for 0 <= e < 2^30, 1 <= m <= 16, magic = 2^34 / m + 1: the excess of
+// magic is at most 1, so e magic / 2^34 exceeds e / m by less than 1 / 16, and
+// e / m lies at least 1 / m below the next whole number (m = 16: magic's excess over 2^30 is
+// exactly 1 and e / 2^34 < 1 / 16).
+__host__ __device__ __forceinline__ uint64_t magic_of(int m) { return ((uint64_t)1 << 34) / m + 1; }
+__device__ __forceinline__ int over_m(int e, uint64_t magic) { return (int)((uint64_t)(uint32_t)e * magic >> 34); }
 
 // acc += A . B on one fragment pair: 16 bytes of each lane's row, 16 (or 8) of
 // the contraction.  A's rows become the accumulator's rows: lane l holds column l % 32 and
@@ -64,21 +93,33 @@ template <> __device__ __forceinline__ uint4 ones<_Float16>() {
     return make_uint4(u, u, u, u);
 }
 
-// 16 bytes of a row from element c on, of `width` elements; zero beyond it.
-// VEC: width and c are multiples of the piece.
-template <typename T, bool VEC> __device__ __forceinline__ uint4 load_piece(const T* row, int c, int width) {
+// 16 bytes of a row from element c on, of `width` elements, at any alignment of
+// the elements; zero beyond the row.  The last, shorter piece of a row is cut out of
+// the row's last 16 bytes.
+template <typename T> __device__ __forceinline__ uint4 load_piece(const T* row, int c, int width) {
     constexpr int E = Vec16<T>::kElems;
-    if constexpr (VEC) {
-        return c < width ? *(const uint4*)(row + c) : make_uint4(0, 0, 0, 0);
-    } else {
-        T t[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            if (c + i < width) t[i] = row[c + i];
-            else from_f32(0.0f, t + i);
+    if (c >= width) return make_uint4(0, 0, 0, 0);
+    if (width >= E) {
+        const int from = min(c, width - E);
+        uint64_t v[2];
+        __builtin_memcpy(v, row + from, 16);
+        const int drop = 8 * (int)sizeof(T) * (c - from);   // bits of the elements before c
+        if (drop != 0) {
+            const bool far = drop >= 64;
+            const int by = drop & 63;
+            const uint64_t lo = far ? v[1] : v[0], hi = far ? 0 : v[1];
+            v[0] = (lo >> by) | (by ? hi << (64 - by) : 0);
+            v[1] = hi >> by;
         }
-        return __builtin_bit_cast(uint4, t);
+        return make_uint4((uint32_t)v[0], (uint32_t)(v[0] >> 32), (uint32_t)v[1], (uint32_t)(v[1] >> 32));
     }
+    T t[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        if (c + i < width) t[i] = row[c + i];
+        else from_f32(0.0f, t + i);
+    }
+    return __builtin_bit_cast(uint4, t);
 }
 
 // Four consecutive outputs of a row from column c on.
@@ -107,10 +148,10 @@ struct RowTile {
     }
 };
 
-// [contraction][128 columns]: rows of 256 or 512 bytes.
-template <typename T> struct ColTile {
+// [contraction][N columns].
+template <typename T, int N> struct ColTile {
     static constexpr int kRows = 128 / (int)sizeof(T);           // contraction elements of a step
-    static constexpr int kPieces = 8 * (int)sizeof(T);           // 16-byte pieces of a row
+    static constexpr int kPieces = N * (int)sizeof(T) / 16;      // 16-byte pieces of a row
     // Pairs of pieces (the 16 columns of a transposed read) move by a number
     // that differs between the 8 rows one read touches.
     __device__ __forceinline__ static int swz(int row) {
@@ -145,9 +186,8 @@ struct LinArgs {
     const int32_t* offsets;
     const int32_t* entry;
     int rows;            // n * m
-    int n;               // points
-    int m;
     int K;
+    uint64_t magic;      // of m
     bool by_slot;
     bool gather;         // rows of a are the points' (entry[s] / m), else by slot
     const void* a;       // x or dy
@@ -157,76 +197,123 @@ struct LinArgs {
     const float* bias;
     void* c;             // y or dx
     int64_t ldc;
+    int row_blocks, col_blocks;
 };
 
 // Row of x behind a slot, or -1.
-__device__ __forceinline__ int64_t source_row(const int32_t* __restrict__ entry, int s, int m, int rows) {
+__device__ __forceinline__ int64_t source_row(const int32_t* __restrict__ entry, int s, uint64_t magic, int rows) {
     const int e = entry[s];
-    return e >= 0 && e < rows ? e / m : -1;
+    return e >= 0 && e < rows ? over_m(e, magic) : -1;
 }
 
-// y = x W^T + b (BACK false) or dx = dy W (BACK true) on one 128 x 128 tile.
-template <typename T, bool VEC, bool BACK>
-__global__ __launch_bounds__(256) void k_linear(const LinArgs a) {
+// Workgroup -> tile.  Workgroups go round the 8 XCDs; consecutive tiles (the columns of a
+// row block, then the next row block of the same list) stay on one, whose L2 then
+// serves the rows to all column blocks and the list's weights to all row blocks.
+__device__ __forceinline__ int tile_of(int block, int tiles) {
+    const int per = (tiles + 7) >> 3;
+    return (block & 7) * per + (block >> 3);
+}
+
+// y = x W^T + b (BACK false) or dx = dy W (BACK true) on one tile.
+template <typename T, bool VEC, bool BACK, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void k_linear(const LinArgs a) {
+    using S = Shape<WM, WN>;
+    using CT = ColTile<T, S::kN>;
     constexpr int E = Vec16<T>::kElems, KS = 8 * E;   // elements of a piece, of a step
-    __shared__ char lds[2][2][kTileBytes] __attribute__((aligned(16)));
-    const ListRows lr = find_rows(a.offsets, a.K, a.rows, blockIdx.x, kTile, a.by_slot);
+    constexpr int AJ = S::kM / 8 / S::kWaves, BJ = S::kN / 8 / S::kWaves;   // wave loads a step
+    constexpr int kStage = S::kABytes + S::kBBytes;
+    __shared__ char lds[2 * kStage] __attribute__((aligned(16)));
+    const int tile = tile_of(blockIdx.x, a.row_blocks * a.col_blocks);
+    if (tile >= a.row_blocks * a.col_blocks) return;
+    const ListRows lr = find_rows(a.offsets, a.K, a.rows, tile / a.col_blocks, S::kM, a.by_slot);
     if (lr.k < 0) return;
     const int kd = BACK ? a.d_out : a.d_in, nd = BACK ? a.d_in : a.d_out;   // contraction, output width
-    const int n0 = blockIdx.y * kTile;
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
+    const int n0 = tile % a.col_blocks * S::kN;
+    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int wm = wave % WM * 64, wn = wave / WM * 64;
     const T* w = (const T*)a.w + (int64_t)lr.k * a.d_in * a.d_out;
 
-    // this thread's four pieces of each operand tile
-    const T* arow[4];
+    // A wave load j covers tile rows 8 (wave AJ + j) .. + 7, 8 pieces each; the
+    // piece that sits at place lane % 8 of a row is lane % 8 ^ row % 8.
+    const int ca = ((lane & 7) ^ (lane >> 3)) * E;
+    const T* pa[AJ];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int s = lr.s0 + (t >> 3) + 32 * j;
+    for (int j = 0; j < AJ; ++j) {
+        const int s = lr.s0 + 8 * (wave * AJ + j) + (lane >> 3);
         int64_t row = -1;
-        if (s < lr.s1) row = a.gather ? source_row(a.entry, s, a.m, a.rows) : s;
-        arow[j] = row >= 0 ? (const T*)a.a + row * a.lda : nullptr;
+        if (s < lr.s1) row = a.gather ? source_row(a.entry, s, a.magic, a.rows) : s;
+        pa[j] = row >= 0 ? (const T*)a.a + row * a.lda : nullptr;
     }
-    uint4 ra[4], rb[4];
-    auto fetch = [&](int k0) {
+    const T* pb[BJ];   // FWD: weight rows; BACK: the first step's pieces
+    int rb[BJ];        // BACK: contraction row within the step
+    constexpr int RI = 64 / CT::kPieces;   // BACK: tile rows of a wave load
+    int cb = ca;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int q = t + 256 * j;
-            ra[j] = arow[j] != nullptr ? load_piece<T, VEC>(arow[j], k0 + (q & 7) * E, kd) : make_uint4(0, 0, 0, 0);
-            if constexpr (!BACK) {
-                const int r = n0 + (q >> 3);
-                rb[j] = r < nd ? load_piece<T, VEC>(w + (int64_t)r * kd, k0 + (q & 7) * E, kd) : make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < BJ; ++j) {
+        if constexpr (!BACK) {
+            const int r = n0 + 8 * (wave * BJ + j) + (lane >> 3);
+            pb[j] = r < nd ? w + (int64_t)r * kd : nullptr;
+        } else {
+            rb[j] = (wave * BJ + j) * RI + lane / CT::kPieces;
+            const int c = n0 + ((lane % CT::kPieces) ^ CT::swz(rb[j])) * E;
+            pb[j] = c < nd ? w + c : nullptr;
+        }
+    }
+    const uint32_t base = lds_address(lds);
+    uint4 ra[VEC ? 1 : AJ], rbv[VEC ? 1 : BJ];
+    // the pieces of the step at k0: VEC into buffer `buf`, else into registers
+    auto fetch = [&](int k0, int buf) {
+        const uint32_t to = base + buf * kStage;
+#pragma unroll
+        for (int j = 0; j < AJ; ++j) {
+            if constexpr (VEC) {
+                const bool ok = pa[j] != nullptr && k0 + ca < kd;
+                fetch_piece(ok ? (const void*)(pa[j] + k0 + ca) : (const void*)&zero_piece, to + (wave * AJ + j) * 1024);
             } else {
-                constexpr int P = ColTile<T>::kPieces;
-                const int r = k0 + q / P;
-                rb[j] = r < kd ? load_piece<T, VEC>(w + (int64_t)r * nd, n0 + (q % P) * E, nd) : make_uint4(0, 0, 0, 0);
+                ra[j] = pa[j] != nullptr ? load_piece<T>(pa[j], k0 + ca, kd) : make_uint4(0, 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < BJ; ++j) {
+            const int r = BACK ? k0 + rb[j] : 0;
+            if constexpr (VEC) {
+                const bool ok = pb[j] != nullptr && (BACK ? r < kd : k0 + cb < kd);
+                const T* p = BACK ? pb[j] + (int64_t)r * nd : pb[j] + k0 + cb;
+                fetch_piece(ok ? (const void*)p : (const void*)&zero_piece, to + S::kABytes + (wave * BJ + j) * 1024);
+            } else if constexpr (BACK) {
+                const int c = n0 + ((lane % CT::kPieces) ^ CT::swz(rb[j])) * E;
+                rbv[j] = r < kd ? load_piece<T>(w + (int64_t)r * nd, c, nd) : make_uint4(0, 0, 0, 0);
+            } else {
+                rbv[j] = pb[j] != nullptr ? load_piece<T>(pb[j], k0 + cb, kd) : make_uint4(0, 0, 0, 0);
             }
         }
     };
     auto put = [&](int buf) {
+        char* to = lds + buf * kStage + lane * 16;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int q = t + 256 * j;
-            *(uint4*)(lds[buf][0] + RowTile::at(q >> 3, q & 7)) = ra[j];
-            constexpr int P = ColTile<T>::kPieces;
-            *(uint4*)(lds[buf][1] + (BACK ? ColTile<T>::at(q / P, q % P) : RowTile::at(q >> 3, q & 7))) = rb[j];
-        }
+        for (int j = 0; j < AJ; ++j) *(uint4*)(to + (wave * AJ + j) * 1024) = ra[j];
+#pragma unroll
+        for (int j = 0; j < BJ; ++j) *(uint4*)(to + S::kABytes + (wave * BJ + j) * 1024) = rbv[j];
     };
 
     f32x16 acc[2][2] = {};
-    fetch(0);
+    fetch(0, 0);
     int buf = 0;
     for (int k0 = 0; k0 < kd; k0 += KS, buf ^= 1) {
-        put(buf);
+        // this step's pieces are in LDS, and every wave has read the last step's
+        if constexpr (VEC) wait_pieces();
+        else put(buf);
         __syncthreads();
-        if (k0 + KS < kd) fetch(k0 + KS);
+        if (k0 + KS < kd) fetch(k0 + KS, buf ^ 1);
+        const char* ta = lds + buf * kStage;
+        const char* tb = ta + S::kABytes;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint4 fa[2], fb[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                fa[i] = RowTile::frag(lds[buf][0], wm + 32 * i, j);
-                fb[i] = BACK ? ColTile<T>::frag(lds[buf][1], wn + 32 * i, j) : RowTile::frag(lds[buf][1], wn + 32 * i, j);
+                fa[i] = RowTile::frag(ta, wm + 32 * i, j);
+                fb[i] = BACK ? CT::frag(tb, wn + 32 * i, j) : RowTile::frag(tb, wn + 32 * i, j);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -237,23 +324,66 @@ __global__ __launch_bounds__(256) void k_linear(const LinArgs a) {
 
     // lane: slot lane % 32, four consecutive outputs per register group
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int s = lr.s0 + wm + 32 * i + (lane & 31);
-        if (s >= lr.s1) continue;
-        T* row = (T*)a.c + (int64_t)s * a.ldc;
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int c = n0 + wn + 32 * h + 8 * q + 4 * (lane >> 5);
-                float v[4];
+        for (int q = 0; q < 4; ++q) {
+            const int c = n0 + wn + 32 * h + 8 * q + 4 * (lane >> 5);
+            if (!BACK && a.bias != nullptr) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    v[e] = acc[i][h][4 * q + e];
-                    if (!BACK && a.bias != nullptr && c + e < nd) v[e] += a.bias[(int64_t)lr.k * nd + c + e];
+                    const float b = c + e < nd ? a.bias[(int64_t)lr.k * nd + c + e] : 0.0f;
+                    acc[0][h][4 * q + e] += b;
+                    acc[1][h][4 * q + e] += b;
                 }
-                store4<T, VEC>(row, c, nd, v);
             }
+        }
+    if constexpr (VEC) {
+        // through LDS, so that a row leaves in whole pieces: the wave's 64 x 64 block, two halves of
+        // 32 rows, pieces swizzled by the row
+        constexpr int RB = 64 * (int)sizeof(T), PR = RB / 16;   // bytes, pieces of a row
+        __syncthreads();
+        char* mine = lds + wave * (32 * RB);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    T v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) from_f32(acc[i][h][4 * q + e], v + e);
+                    const int r = lane & 31, c = (32 * h + 8 * q + 4 * (lane >> 5)) * (int)sizeof(T);
+                    __builtin_memcpy(__builtin_assume_aligned(mine + r * RB + (((c >> 4) ^ (r & (PR - 1))) << 4) + (c & 15),
+                                                              4 * sizeof(T)), v, 4 * sizeof(T));
+                }
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int u = 0; u < 32 * PR / 64; ++u) {
+                const int r = (64 / PR) * u + lane / PR, p = lane % PR;
+                const uint4 v = *(const uint4*)(mine + r * RB + ((p ^ (r & (PR - 1))) << 4));
+                const int s = lr.s0 + wm + 32 * i + r, c = n0 + wn + p * E;
+                if (s < lr.s1 && c < nd) *(uint4*)((T*)a.c + (int64_t)s * a.ldc + c) = v;
+            }
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int s = lr.s0 + wm + 32 * i + (lane & 31);
+            if (s >= lr.s1) continue;
+            T* row = (T*)a.c + (int64_t)s * a.ldc;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = acc[i][h][4 * q + e];
+                    store4<T, false>(row, n0 + wn + 32 * h + 8 * q + 4 * (lane >> 5), nd, v);
+                }
+        }
     }
 }
 
@@ -262,7 +392,8 @@ __global__ __launch_bounds__(256) void k_linear(const LinArgs a) {
 struct GradArgs {
     const int32_t* offsets;
     const int32_t* entry;
-    int rows, m, K;
+    int rows, K;
+    uint64_t magic;
     bool by_slot, gather;
     int chunk;              // rows of a list one workgroup sums
     const void* x;
@@ -273,6 +404,7 @@ struct GradArgs {
     float* dw;
     float* db;
     float* part;            // slots of d_out * d_in + d_out sums
+    int row_blocks, in_blocks, out_blocks;
 };
 
 // First partial slot of a list of more than one chunk that starts at slot a:
@@ -280,52 +412,93 @@ struct GradArgs {
 // since floor(2 b / chunk) - floor(2 a / chunk) >= ceil(2 c / chunk) - 1 >= ceil(c / chunk) for c > chunk.
 __device__ __host__ __forceinline__ int64_t first_slot(int64_t a, int chunk) { return 2 * a / chunk; }
 
-// dW (and db) over one chunk of one list, a 128 (d_out) x 128 (d_in) tile.
-template <typename T, bool VEC>
-__global__ __launch_bounds__(256) void k_linear_dw(const GradArgs a) {
-    constexpr int E = Vec16<T>::kElems, P = ColTile<T>::kPieces, KS = ColTile<T>::kRows;
-    __shared__ char lds[2][2][kTileBytes] __attribute__((aligned(16)));
-    const ListRows lr = find_rows(a.offsets, a.K, a.rows, blockIdx.z, a.chunk, a.by_slot);
+// dW (and db) over one chunk of one list, one tile: 64 WM of d_in x 64 WN of d_out.
+template <typename T, bool VEC, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void k_linear_dw(const GradArgs a) {
+    using S = Shape<WM, WN>;
+    using XT = ColTile<T, S::kM>;
+    using YT = ColTile<T, S::kN>;
+    constexpr int E = Vec16<T>::kElems, KS = XT::kRows;
+    constexpr int XJ = S::kM / 8 / S::kWaves, YJ = S::kN / 8 / S::kWaves;
+    constexpr int XR = 64 / XT::kPieces, YR = 64 / YT::kPieces;   // tile rows of a wave load
+    constexpr int kStage = S::kABytes + S::kBBytes;
+    __shared__ char lds[2 * kStage] __attribute__((aligned(16)));
+    const int per_row = a.in_blocks * a.out_blocks;
+    const int tile = tile_of(blockIdx.x, a.row_blocks * per_row);
+    if (tile >= a.row_blocks * per_row) return;
+    const ListRows lr = find_rows(a.offsets, a.K, a.rows, tile / per_row, a.chunk, a.by_slot);
     if (lr.k < 0) return;
-    const int i0 = blockIdx.x * kTile, o0 = blockIdx.y * kTile;
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    const int wi = (wave & 1) * 64, wo = (wave >> 1) * 64;
+    const int i0 = tile % a.in_blocks * S::kM, o0 = tile % per_row / a.in_blocks * S::kN;
+    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int wi = wave % WM * 64, wo = wave / WM * 64;
     const int first = clamped_offset(a.offsets, lr.k, a.rows);
     const int s1 = min((int64_t)lr.s0 + a.chunk, (int64_t)lr.s1);
-    const bool with_db = a.db != nullptr && blockIdx.x == 0 && wi == 0;
+    const bool with_db = a.db != nullptr && i0 == 0 && wi == 0;
 
-    uint4 rx[4], ry[4];
-    auto fetch = [&](int s0) {
+    const uint32_t base = lds_address(lds);
+    uint4 rx[VEC ? 1 : XJ], ry[VEC ? 1 : YJ];
+    int from[XJ];   // rows of x behind this lane's slots of a step, -1: none
+    auto sources = [&](int s0) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int q = t + 256 * j, s = s0 + q / P;
-            rx[j] = ry[j] = make_uint4(0, 0, 0, 0);
-            if (s < s1) {
-                const int64_t row = a.gather ? source_row(a.entry, s, a.m, a.rows) : s;
-                if (row >= 0) rx[j] = load_piece<T, VEC>((const T*)a.x + row * a.ldx, i0 + (q % P) * E, a.d_in);
-                ry[j] = load_piece<T, VEC>((const T*)a.dy + (int64_t)s * a.ldy, o0 + (q % P) * E, a.d_out);
-            }
+        for (int j = 0; j < XJ; ++j) {
+            const int s = s0 + (wave * XJ + j) * XR + lane / XT::kPieces;
+            from[j] = -1;
+            if (s < s1) from[j] = a.gather ? (int)source_row(a.entry, s, a.magic, a.rows) : s;
         }
     };
+    auto fetch = [&](int s0, int buf) {
+        const uint32_t to = base + buf * kStage;
+#pragma unroll
+        for (int j = 0; j < XJ; ++j) {
+            const int r = (wave * XJ + j) * XR + lane / XT::kPieces;
+            const int c = i0 + ((lane % XT::kPieces) ^ XT::swz(r)) * E;
+            const T* row = (const T*)a.x + (int64_t)from[j] * a.ldx;
+            if constexpr (VEC)
+                fetch_piece(from[j] >= 0 && c < a.d_in ? (const void*)(row + c) : (const void*)&zero_piece,
+                            to + (wave * XJ + j) * 1024);
+            else rx[j] = from[j] >= 0 ? load_piece<T>(row, c, a.d_in) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < YJ; ++j) {
+            const int r = (wave * YJ + j) * YR + lane / YT::kPieces, s = s0 + r;
+            const int c = o0 + ((lane % YT::kPieces) ^ YT::swz(r)) * E;
+            const T* row = (const T*)a.dy + (int64_t)s * a.ldy;
+            if constexpr (VEC)
+                fetch_piece(s < s1 && c < a.d_out ? (const void*)(row + c) : (const void*)&zero_piece,
+                            to + S::kABytes + (wave * YJ + j) * 1024);
+            else ry[j] = s < s1 ? load_piece<T>(row, c, a.d_out) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    auto put = [&](int buf) {
+        char* to = lds + buf * kStage + lane * 16;
+#pragma unroll
+        for (int j = 0; j < XJ; ++j) *(uint4*)(to + (wave * XJ + j) * 1024) = rx[j];
+#pragma unroll
+        for (int j = 0; j < YJ; ++j) *(uint4*)(to + S::kABytes + (wave * YJ + j) * 1024) = ry[j];
+    };
+
     f32x16 acc[2][2] = {}, sum[2] = {};
-    fetch(lr.s0);
+    sources(lr.s0);
+    fetch(lr.s0, 0);
+    sources(lr.s0 + KS);
     int buf = 0;
     for (int s0 = lr.s0; s0 < s1; s0 += KS, buf ^= 1) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int q = t + 256 * j;
-            *(uint4*)(lds[buf][0] + ColTile<T>::at(q / P, q % P)) = rx[j];
-            *(uint4*)(lds[buf][1] + ColTile<T>::at(q / P, q % P)) = ry[j];
-        }
+        if constexpr (VEC) wait_pieces();
+        else put(buf);
         __syncthreads();
-        if (s0 + KS < s1) fetch(s0 + KS);
+        if (s0 + KS < s1) {
+            fetch(s0 + KS, buf ^ 1);
+            sources(s0 + 2 * KS);
+        }
+        const char* tx = lds + buf * kStage;
+        const char* ty = tx + S::kABytes;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint4 fx[2], fy[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                fx[i] = ColTile<T>::frag(lds[buf][0], wi + 32 * i, j);
-                fy[i] = ColTile<T>::frag(lds[buf][1], wo + 32 * i, j);
+                fx[i] = XT::frag(tx, wi + 32 * i, j);
+                fy[i] = YT::frag(ty, wo + 32 * i, j);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -358,7 +531,7 @@ __global__ __launch_bounds__(256) void k_linear_dw(const GradArgs a) {
                 float v[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = acc[i][h][4 * q + e];
-                store4<float, false>(dw + (int64_t)o * a.d_in, c, a.d_in, v);
+                store4<float, VEC>(dw + (int64_t)o * a.d_in, c, a.d_in, v);
             }
     }
 }
@@ -386,6 +559,8 @@ __global__ __launch_bounds__(256) void k_zero(float* p, int64_t n) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0.0f;
 }
 
+constexpr int kTile = 128;   // rows and columns of a tile: 2 x 2 waves
+
 // Rows of a list per workgroup of the weights' gradient: about 1024
 // workgroups over all tiles, at least 512 rows.
 int chunk_rows(int64_t rows, const gmm_linear_desc* d) {
@@ -396,6 +571,8 @@ int chunk_rows(int64_t rows, const gmm_linear_desc* d) {
     return (int)(chunk > most ? most : chunk);
 }
 
+int blocks_of(int width) { return (width + kTile - 1) / kTile; }
+
 gmm_status check_desc(const gmm_linear_desc* d) {
     if (d == nullptr) return GMM_E_ARG;
     gmm_status st = check_width(d->d_in, d->dtype);
@@ -404,11 +581,21 @@ gmm_status check_desc(const gmm_linear_desc* d) {
     return st;
 }
 
+// Tiles of a launch, or GMM_E_ARG where they do not fit a grid.
+gmm_status grid_of(int64_t tiles, int* grid) {
+    if (tiles > ((int64_t)1 << 24) - 8) return GMM_E_ARG;   // a grid holds fewer than 2^32 threads
+    *grid = (int)((tiles + 7) / 8 * 8);
+    return GMM_OK;
+}
+
 template <typename T, bool VEC, bool BACK> gmm_status launch_linear(const LinArgs& a, int64_t k, hipStream_t stream) {
     LinArgs b = a;
-    const int64_t blocks = row_blocks(a.rows, k, kTile, &b.by_slot);
-    const int nd = BACK ? a.d_in : a.d_out;
-    hipLaunchKernelGGL((k_linear<T, VEC, BACK>), dim3(blocks, (nd + kTile - 1) / kTile), dim3(256), 0, stream, b);
+    int grid;
+    b.row_blocks = (int)row_blocks(a.rows, k, kTile, &b.by_slot);
+    b.col_blocks = blocks_of(BACK ? a.d_in : a.d_out);
+    const gmm_status st = grid_of((int64_t)b.row_blocks * b.col_blocks, &grid);
+    if (st != GMM_OK) return st;
+    hipLaunchKernelGGL((k_linear<T, VEC, BACK, 2, 2>), dim3(grid), dim3(256), 0, stream, b);
     return launched();
 }
 
@@ -426,9 +613,12 @@ template <bool BACK> gmm_status run_linear(const LinArgs& a, int64_t k, int dtyp
 
 template <typename T, bool VEC> gmm_status launch_dw(const GradArgs& a, hipStream_t stream) {
     GradArgs b = a;
-    const int64_t blocks = row_blocks(a.rows, a.K, a.chunk, &b.by_slot);
-    const dim3 grid((a.d_in + kTile - 1) / kTile, (a.d_out + kTile - 1) / kTile, blocks);
-    hipLaunchKernelGGL((k_linear_dw<T, VEC>), grid, dim3(256), 0, stream, b);
+    int grid;
+    b.row_blocks = (int)row_blocks(a.rows, a.K, a.chunk, &b.by_slot);
+    b.in_blocks = blocks_of(a.d_in), b.out_blocks = blocks_of(a.d_out);
+    const gmm_status st = grid_of((int64_t)b.row_blocks * b.in_blocks * b.out_blocks, &grid);
+    if (st != GMM_OK) return st;
+    hipLaunchKernelGGL((k_linear_dw<T, VEC, 2, 2>), dim3(grid), dim3(256), 0, stream, b);
     const int64_t wide = (int64_t)a.d_out * a.d_in;
     const int64_t parts = (wide + a.d_out + 1023) / 1024;
     hipLaunchKernelGGL(k_linear_dw_join, dim3(parts < 256 ? parts : 256, a.K), dim3(256), 0, stream, b);
@@ -452,8 +642,8 @@ gmm_status gmm_linear(const gmm_routes* routes, const gmm_linear_desc* desc, con
         return st;
     if (routes->n == 0) return GMM_OK;
     if (x == nullptr || w == nullptr || y == nullptr) return GMM_E_ARG;
-    LinArgs a = {routes->offsets, routes->entry, (int)(routes->n * routes->m), (int)routes->n, routes->m, routes->k,
-                 false, desc->sorted_rows == 0, x, desc->ldx, w, (int)desc->d_in, (int)desc->d_out, bias, y, desc->ldy};
+    LinArgs a = {routes->offsets, routes->entry, (int)(routes->n * routes->m), routes->k, magic_of(routes->m), false,
+                 desc->sorted_rows == 0, x, desc->ldx, w, (int)desc->d_in, (int)desc->d_out, bias, y, desc->ldy, 0, 0};
     const int es = elem_size(desc->dtype);
     const bool vec = desc->d_in * es % 16 == 0 && desc->ldx * es % 16 == 0 && aligned16(x) && aligned16(w) &&
                      desc->d_out * es % 16 == 0 && desc->ldy * es % 16 == 0 && aligned16(y);
@@ -496,8 +686,8 @@ gmm_status gmm_linear_backward(const gmm_routes* routes, const gmm_linear_desc* 
     const bool wide = desc->d_in * es % 16 == 0 && desc->d_out * es % 16 == 0;
     const bool dy_vec = desc->ldy * es % 16 == 0 && aligned16(dy);
     if (dx != nullptr && rows > 0) {
-        LinArgs a = {routes->offsets, routes->entry, (int)rows, (int)routes->n, routes->m, routes->k, false, false, dy,
-                     desc->ldy, w, (int)desc->d_in, (int)desc->d_out, nullptr, dx, desc->lddx};
+        LinArgs a = {routes->offsets, routes->entry, (int)rows, routes->k, magic_of(routes->m), false, false, dy,
+                     desc->ldy, w, (int)desc->d_in, (int)desc->d_out, nullptr, dx, desc->lddx, 0, 0};
         const bool vec = wide && dy_vec && aligned16(w) && desc->lddx * es % 16 == 0 && aligned16(dx);
         if ((st = run_linear<true>(a, routes->k, desc->dtype, vec, stream)) != GMM_OK) return st;
     }
@@ -508,10 +698,10 @@ gmm_status gmm_linear_backward(const gmm_routes* routes, const gmm_linear_desc* 
         if (db != nullptr) hipLaunchKernelGGL(k_zero, dim3(64), dim3(256), 0, stream, db, per);
         return launched();
     }
-    GradArgs g = {routes->offsets, routes->entry, (int)rows, routes->m, routes->k, false, desc->sorted_rows == 0,
-                  chunk_rows(rows, desc), x, desc->ldx, dy, desc->ldy, (int)desc->d_in, (int)desc->d_out, dw, db,
-                  (float*)ws};
-    const bool vec = wide && dy_vec && desc->ldx * es % 16 == 0 && aligned16(x);
+    GradArgs g = {routes->offsets, routes->entry, (int)rows, routes->k, magic_of(routes->m), false,
+                  desc->sorted_rows == 0, chunk_rows(rows, desc), x, desc->ldx, dy, desc->ldy, (int)desc->d_in,
+                  (int)desc->d_out, dw, db, (float*)ws, 0, 0, 0};
+    const bool vec = wide && dy_vec && desc->ldx * es % 16 == 0 && aligned16(x) && aligned16(dw);
     switch (desc->dtype) {
         case GMM_F32: return vec ? launch_dw<float, true>(g, stream) : launch_dw<float, false>(g, stream);
         case GMM_BF16: return vec ? launch_dw<bf16_t, true>(g, stream) : launch_dw<bf16_t, false>(g, stream);

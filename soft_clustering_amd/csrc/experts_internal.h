@@ -29,12 +29,13 @@ template <typename T> __device__ __forceinline__ uint4 pack16(const float* v) {
 // t0_{k+1}, so rows / BM + K blocks cover every list without any host
 // knowledge of the lengths), or, with by_slot, the block that starts at slot
 // t (only every BM-th slot of a list starts one; fewer workgroups where there are
-// fewer rows than lists).  One wave finds k in two steps of 64 candidates.
-// Every offset is clamped to [0, rows]: whatever the array holds, the slots
-// stay inside the row buffers.
+// fewer rows than lists).  Each wave finds k for itself: 256 candidates at once, four a
+// lane, after a first step over every 64th list where there are more.  Every offset is
+// clamped to [0, rows]: whatever the array holds, the slots stay inside the row buffers.
 struct ListRows {
     int k;        // list, -1: nothing to do
-    int s0, s1;   // slots [s0, s1)
+    int s0, s1;   // slots [s0, s1): from the block's first to the list's end
+    int first;    // the list's first slot
 };
 
 __device__ __forceinline__ int clamped_offset(const int32_t* offsets, int k, int rows) {
@@ -44,31 +45,42 @@ __device__ __forceinline__ int clamped_offset(const int32_t* offsets, int k, int
 __device__ __forceinline__ ListRows find_rows(const int32_t* __restrict__ offsets, int K, int rows, int t,
                                               int bm, bool by_slot) {
     const int lane = threadIdx.x & 63;
-    auto before = [&](int k) {   // does list k start at or before block t
-        if (k >= K) return false;
-        const int o = clamped_offset(offsets, k, rows);
-        return (by_slot ? o : o / bm + k) <= t;
+    auto before = [&](int k, int o) { return k < K && (by_slot ? o : o / bm + k) <= t; };   // list k starts by block t
+    int k0 = 0;
+    if (K > 256) {
+        const int k = lane * 64;
+        const int o = clamped_offset(offsets, min(k, K), rows);
+        k0 = max(__popcll(__ballot(before(k, o))) - 1, 0) * 64;
+    }
+    int o[4], count = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) o[q] = clamped_offset(offsets, min(k0 + 4 * lane + q, K), rows);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) count += __popcll(__ballot(before(k0 + 4 * lane + q, o[q])));
+    const int i = __builtin_amdgcn_readfirstlane(count) - 1;   // the list is k0 + i
+    ListRows r = {-1, 0, 0, 0};
+    if (i < 0) return r;
+    auto window = [&](int at) {
+        const int l = at >> 2, q = at & 3;
+        const int lo = q & 1 ? __builtin_amdgcn_readlane(o[1], l) : __builtin_amdgcn_readlane(o[0], l);
+        const int hi = q & 1 ? __builtin_amdgcn_readlane(o[3], l) : __builtin_amdgcn_readlane(o[2], l);
+        return q & 2 ? hi : lo;
     };
-    int seg = 0;
-    if (K > 64) seg = max(__popcll(__ballot(before(lane * 64))) - 1, 0);
-    int k = seg * 64 + __popcll(__ballot(before(seg * 64 + lane))) - 1;
-    k = __builtin_amdgcn_readfirstlane(k);
-    ListRows r = {-1, 0, 0};
-    if (k < 0 || k >= K) return r;
-    const int a = clamped_offset(offsets, k, rows), b = clamped_offset(offsets, k + 1, rows);
+    const int a = window(i), b = i < 255 ? window(i + 1) : clamped_offset(offsets, min(k0 + 256, K), rows);
     int s0;
     if (by_slot) {
         if ((t - a) % bm != 0) return r;
         s0 = t;
     } else {
-        const int64_t first = a + (int64_t)(t - (a / bm + k)) * bm;
-        if (first >= b) return r;
-        s0 = (int)first;
+        const int64_t start = a + (int64_t)(t - (a / bm + k0 + i)) * bm;
+        if (start >= b) return r;
+        s0 = (int)start;
     }
     if (s0 >= b) return r;
-    r.k = k;
+    r.k = k0 + i;
     r.s0 = __builtin_amdgcn_readfirstlane(s0);
     r.s1 = __builtin_amdgcn_readfirstlane(b);
+    r.first = __builtin_amdgcn_readfirstlane(a);
     return r;
 }
 

@@ -33,11 +33,17 @@ typedef short short4v __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) short4v lds_short4;
 typedef __attribute__((address_space(3))) char lds_char;
 
+constexpr int kStep = 64;      // bytes of the contraction a step
+constexpr int kFrags = kStep / 32;   // fragments of a step
+constexpr int kStages = 3;     // steps in LDS: one multiplied, the others on their way
+
 // Waves of a workgroup along the rows and along the columns of its tile.
 template <int WM, int WN> struct Shape {
     static constexpr int kThreads = 64 * WM * WN, kM = 64 * WM, kN = 64 * WN;
-    static constexpr int kABytes = kM * 128, kBBytes = kN * 128;   // one operand, one step
+    static constexpr int kABytes = kM * kStep, kBBytes = kN * kStep;   // one operand, one step
+    static constexpr int kStage = kABytes + kBBytes;
     static constexpr int kWaves = WM * WN;
+    static constexpr int kAJ = kABytes / 1024 / kWaves, kBJ = kBBytes / 1024 / kWaves;   // wave loads a step
 };
 
 __device__ __constant__ uint4 zero_piece = {0, 0, 0, 0};
@@ -49,7 +55,7 @@ __device__ __constant__ uint4 zero_piece = {0, 0, 0, 0};
 __device__ __forceinline__ void fetch_piece(const void* g, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(g) : "memory", "m0");
 }
-__device__ __forceinline__ void wait_pieces() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+template <int N> __device__ __forceinline__ void wait_pieces() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
     return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p);
 }
@@ -138,10 +144,13 @@ template <typename T, bool VEC> __device__ __forceinline__ void store4(T* row, i
 
 // ---- operand tiles in LDS
 
-// [row][128 bytes]: piece p of a row sits at p ^ (row & 7).
+// [row][kStep bytes]: pieces XOR-swizzled so that the 8 rows that one LDS cycle of
+// a fragment read touches lie in 8 different places of the 256 bytes of banks.
 struct RowTile {
-    __device__ __forceinline__ static int at(int row, int piece) { return row * 128 + ((piece ^ (row & 7)) << 4); }
-    // lane's fragment of step j (of four) for row block `r0`
+    static constexpr int kPieces = kStep / 16, kRowsPerLoad = 64 / kPieces;
+    __device__ __forceinline__ static int swz(int row) { return kPieces == 8 ? row & 7 : (row >> 2) & 3; }
+    __device__ __forceinline__ static int at(int row, int piece) { return row * kStep + ((piece ^ swz(row)) << 4); }
+    // lane's fragment j of the step for row block `r0`
     __device__ __forceinline__ static uint4 frag(const char* t, int r0, int j) {
         const int lane = threadIdx.x & 63;
         return *(const uint4*)(t + at(r0 + (lane & 31), 2 * j + (lane >> 5)));
@@ -150,7 +159,7 @@ struct RowTile {
 
 // [contraction][N columns].
 template <typename T, int N> struct ColTile {
-    static constexpr int kRows = 128 / (int)sizeof(T);           // contraction elements of a step
+    static constexpr int kRows = kStep / (int)sizeof(T);         // contraction elements of a step
     static constexpr int kPieces = N * (int)sizeof(T) / 16;      // 16-byte pieces of a row
     // Pairs of pieces (the 16 columns of a transposed read) move by a number
     // that differs between the 8 rows one read touches.
@@ -200,9 +209,8 @@ struct LinArgs {
     int row_blocks, col_blocks;
 };
 
-// Row of x behind a slot, or -1.
-__device__ __forceinline__ int64_t source_row(const int32_t* __restrict__ entry, int s, uint64_t magic, int rows) {
-    const int e = entry[s];
+// Row of x behind an entry, or -1.
+__device__ __forceinline__ int source_row(int e, uint64_t magic, int rows) {
     return e >= 0 && e < rows ? over_m(e, magic) : -1;
 }
 
@@ -216,13 +224,13 @@ __device__ __forceinline__ int tile_of(int block, int tiles) {
 
 // y = x W^T + b (BACK false) or dx = dy W (BACK true) on one tile.
 template <typename T, bool VEC, bool BACK, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN) void k_linear(const LinArgs a) {
+__global__ __launch_bounds__(64 * WM * WN, 3) void k_linear(const LinArgs a) {
     using S = Shape<WM, WN>;
     using CT = ColTile<T, S::kN>;
-    constexpr int E = Vec16<T>::kElems, KS = 8 * E;   // elements of a piece, of a step
-    constexpr int AJ = S::kM / 8 / S::kWaves, BJ = S::kN / 8 / S::kWaves;   // wave loads a step
-    constexpr int kStage = S::kABytes + S::kBBytes;
-    __shared__ char lds[2 * kStage] __attribute__((aligned(16)));
+    constexpr int E = Vec16<T>::kElems, KS = kStep / (int)sizeof(T);   // elements of a piece, of a step
+    constexpr int AJ = S::kAJ, BJ = S::kBJ, kStage = S::kStage;
+    constexpr int kOut = S::kWaves * 32 * 64 * (int)sizeof(T);   // the epilogue's rows
+    __shared__ char lds[kStages * kStage > kOut ? kStages * kStage : kOut] __attribute__((aligned(16)));
     const int tile = tile_of(blockIdx.x, a.row_blocks * a.col_blocks);
     if (tile >= a.row_blocks * a.col_blocks) return;
     const ListRows lr = find_rows(a.offsets, a.K, a.rows, tile / a.col_blocks, S::kM, a.by_slot);
@@ -233,16 +241,21 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear(const LinArgs a) {
     const int wm = wave % WM * 64, wn = wave / WM * 64;
     const T* w = (const T*)a.w + (int64_t)lr.k * a.d_in * a.d_out;
 
-    // A wave load j covers tile rows 8 (wave AJ + j) .. + 7, 8 pieces each; the
-    // piece that sits at place lane % 8 of a row is lane % 8 ^ row % 8.
-    const int ca = ((lane & 7) ^ (lane >> 3)) * E;
+    // Wave load j covers the RA tile rows from RA (wave AJ + j) on; the piece that sits at
+    // place p of a row is p ^ swz(row), the same for every j (RA rows are a whole period).
+    constexpr int PA = RowTile::kPieces, RA = RowTile::kRowsPerLoad;
+    const int ca = ((lane % PA) ^ RowTile::swz(lane / PA)) * E;
     const T* pa[AJ];
+    int e[AJ];
+    if (a.gather) {
+#pragma unroll
+        for (int j = 0; j < AJ; ++j) e[j] = a.entry[min(lr.s0 + RA * (wave * AJ + j) + lane / PA, lr.s1 - 1)];
+    }
 #pragma unroll
     for (int j = 0; j < AJ; ++j) {
-        const int s = lr.s0 + 8 * (wave * AJ + j) + (lane >> 3);
-        int64_t row = -1;
-        if (s < lr.s1) row = a.gather ? source_row(a.entry, s, a.magic, a.rows) : s;
-        pa[j] = row >= 0 ? (const T*)a.a + row * a.lda : nullptr;
+        const int s = lr.s0 + RA * (wave * AJ + j) + lane / PA;
+        const int row = a.gather ? source_row(e[j], a.magic, a.rows) : s;
+        pa[j] = s < lr.s1 && row >= 0 ? (const T*)a.a + (int64_t)row * a.lda : nullptr;
     }
     const T* pb[BJ];   // FWD: weight rows; BACK: the first step's pieces
     int rb[BJ];        // BACK: contraction row within the step
@@ -251,7 +264,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear(const LinArgs a) {
 #pragma unroll
     for (int j = 0; j < BJ; ++j) {
         if constexpr (!BACK) {
-            const int r = n0 + 8 * (wave * BJ + j) + (lane >> 3);
+            const int r = n0 + RA * (wave * BJ + j) + lane / PA;
             pb[j] = r < nd ? w + (int64_t)r * kd : nullptr;
         } else {
             rb[j] = (wave * BJ + j) * RI + lane / CT::kPieces;
@@ -296,19 +309,44 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear(const LinArgs a) {
         for (int j = 0; j < BJ; ++j) *(uint4*)(to + S::kABytes + (wave * BJ + j) * 1024) = rbv[j];
     };
 
+    const bool live[2] = {n0 + wn < nd, n0 + wn + 32 < nd};   // blocks of columns with outputs
     f32x16 acc[2][2] = {};
-    fetch(0, 0);
+    if (!BACK && a.bias != nullptr) {   // sums start from the bias
+        const float* bias = a.bias + (int64_t)lr.k * nd;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int c = n0 + wn + 32 * h + 8 * q + 4 * (lane >> 5);
+                float b[4];
+                if constexpr (VEC) {
+                    __builtin_memcpy(b, bias + (c < nd ? c : 0), sizeof(b));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) b[e] = bias[min(c + e, nd - 1)];
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[0][h][4 * q + e] = acc[1][h][4 * q + e] = b[e];
+            }
+    }
+    const int steps = (kd + KS - 1) / KS;
+    constexpr int kAhead = VEC ? kStages - 1 : 1;   // steps on their way (registers hold one)
+    for (int i = 0; i < kAhead && i < steps; ++i) fetch(i * KS, i);
     int buf = 0;
-    for (int k0 = 0; k0 < kd; k0 += KS, buf ^= 1) {
+    for (int i = 0; i < steps; ++i) {
         // this step's pieces are in LDS, and every wave has read the last step's
-        if constexpr (VEC) wait_pieces();
-        else put(buf);
+        if constexpr (VEC) {
+            if (i + kAhead - 1 < steps) wait_pieces<(kAhead - 1) * (AJ + BJ)>();
+            else wait_pieces<0>();
+        } else {
+            put(buf);
+        }
         __syncthreads();
-        if (k0 + KS < kd) fetch(k0 + KS, buf ^ 1);
+        if (i + kAhead < steps) fetch((i + kAhead) * KS, buf + kAhead < kStages ? buf + kAhead : buf + kAhead - kStages);
         const char* ta = lds + buf * kStage;
         const char* tb = ta + S::kABytes;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kFrags; ++j) {
             uint4 fa[2], fb[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -316,27 +354,16 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear(const LinArgs a) {
                 fb[i] = BACK ? CT::frag(tb, wn + 32 * i, j) : RowTile::frag(tb, wn + 32 * i, j);
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int h = 0; h < 2; ++h)
+                if (live[h]) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) acc[i][h] = mma<T>(fb[h], fa[i], acc[i][h]);
+                    for (int i = 0; i < 2; ++i) acc[i][h] = mma<T>(fb[h], fa[i], acc[i][h]);
+                }
         }
+        buf = buf + 1 < kStages ? buf + 1 : 0;
     }
 
     // lane: slot lane % 32, four consecutive outputs per register group
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int c = n0 + wn + 32 * h + 8 * q + 4 * (lane >> 5);
-            if (!BACK && a.bias != nullptr) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float b = c + e < nd ? a.bias[(int64_t)lr.k * nd + c + e] : 0.0f;
-                    acc[0][h][4 * q + e] += b;
-                    acc[1][h][4 * q + e] += b;
-                }
-            }
-        }
     if constexpr (VEC) {
         // through LDS, so that a row leaves in whole pieces: the wave's 64 x 64 block, two halves of
         // 32 rows, pieces swizzled by the row
@@ -358,13 +385,18 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear(const LinArgs a) {
                 }
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
+            constexpr int U = 32 * PR / 64, RU = 64 / PR;
+            uint4 v[U];
 #pragma unroll
-            for (int u = 0; u < 32 * PR / 64; ++u) {
-                const int r = (64 / PR) * u + lane / PR, p = lane % PR;
-                const uint4 v = *(const uint4*)(mine + r * RB + ((p ^ (r & (PR - 1))) << 4));
-                const int s = lr.s0 + wm + 32 * i + r, c = n0 + wn + p * E;
-                if (s < lr.s1 && c < nd) *(uint4*)((T*)a.c + (int64_t)s * a.ldc + c) = v;
+            for (int u = 0; u < U; ++u) {
+                const int r = RU * u + lane / PR;
+                v[u] = *(const uint4*)(mine + r * RB + (((lane % PR) ^ (r & (PR - 1))) << 4));
             }
+            const int s = lr.s0 + wm + 32 * i + lane / PR, c = n0 + wn + lane % PR * E;
+            T* to = (T*)a.c + (int64_t)s * a.ldc + c;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (s + RU * u < lr.s1 && c < nd) *(uint4*)(to + (int64_t)(RU * u) * a.ldc) = v[u];
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
         }
@@ -414,15 +446,14 @@ __device__ __host__ __forceinline__ int64_t first_slot(int64_t a, int chunk) { r
 
 // dW (and db) over one chunk of one list, one tile: 64 WM of d_in x 64 WN of d_out.
 template <typename T, bool VEC, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN) void k_linear_dw(const GradArgs a) {
+__global__ __launch_bounds__(64 * WM * WN, 3) void k_linear_dw(const GradArgs a) {
     using S = Shape<WM, WN>;
     using XT = ColTile<T, S::kM>;
     using YT = ColTile<T, S::kN>;
     constexpr int E = Vec16<T>::kElems, KS = XT::kRows;
-    constexpr int XJ = S::kM / 8 / S::kWaves, YJ = S::kN / 8 / S::kWaves;
+    constexpr int XJ = S::kAJ, YJ = S::kBJ, kStage = S::kStage;
     constexpr int XR = 64 / XT::kPieces, YR = 64 / YT::kPieces;   // tile rows of a wave load
-    constexpr int kStage = S::kABytes + S::kBBytes;
-    __shared__ char lds[2 * kStage] __attribute__((aligned(16)));
+    __shared__ char lds[kStages * kStage] __attribute__((aligned(16)));
     const int per_row = a.in_blocks * a.out_blocks;
     const int tile = tile_of(blockIdx.x, a.row_blocks * per_row);
     if (tile >= a.row_blocks * per_row) return;
@@ -431,7 +462,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear_dw(const GradArgs a) {
     const int i0 = tile % a.in_blocks * S::kM, o0 = tile % per_row / a.in_blocks * S::kN;
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wi = wave % WM * 64, wo = wave / WM * 64;
-    const int first = clamped_offset(a.offsets, lr.k, a.rows);
+    const int first = lr.first;
     const int s1 = min((int64_t)lr.s0 + a.chunk, (int64_t)lr.s1);
     const bool with_db = a.db != nullptr && i0 == 0 && wi == 0;
 
@@ -439,11 +470,15 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear_dw(const GradArgs a) {
     uint4 rx[VEC ? 1 : XJ], ry[VEC ? 1 : YJ];
     int from[XJ];   // rows of x behind this lane's slots of a step, -1: none
     auto sources = [&](int s0) {
+        int e[XJ];
+        if (a.gather) {
+#pragma unroll
+            for (int j = 0; j < XJ; ++j) e[j] = a.entry[min(s0 + (wave * XJ + j) * XR + lane / XT::kPieces, s1 - 1)];
+        }
 #pragma unroll
         for (int j = 0; j < XJ; ++j) {
             const int s = s0 + (wave * XJ + j) * XR + lane / XT::kPieces;
-            from[j] = -1;
-            if (s < s1) from[j] = a.gather ? (int)source_row(a.entry, s, a.magic, a.rows) : s;
+            from[j] = s < s1 ? a.gather ? source_row(e[j], a.magic, a.rows) : s : -1;
         }
     };
     auto fetch = [&](int s0, int buf) {
@@ -477,23 +512,32 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear_dw(const GradArgs a) {
         for (int j = 0; j < YJ; ++j) *(uint4*)(to + S::kABytes + (wave * YJ + j) * 1024) = ry[j];
     };
 
+    const bool live[2] = {i0 + wi < a.d_in, i0 + wi + 32 < a.d_in};   // blocks with gradients
     f32x16 acc[2][2] = {}, sum[2] = {};
-    sources(lr.s0);
-    fetch(lr.s0, 0);
-    sources(lr.s0 + KS);
+    const int steps = (s1 - lr.s0 + KS - 1) / KS;
+    constexpr int kAhead = VEC ? kStages - 1 : 1;
+    for (int i = 0; i < kAhead && i < steps; ++i) {
+        sources(lr.s0 + i * KS);
+        fetch(lr.s0 + i * KS, i);
+    }
+    sources(lr.s0 + kAhead * KS);
     int buf = 0;
-    for (int s0 = lr.s0; s0 < s1; s0 += KS, buf ^= 1) {
-        if constexpr (VEC) wait_pieces();
-        else put(buf);
+    for (int i = 0; i < steps; ++i) {
+        if constexpr (VEC) {
+            if (i + kAhead - 1 < steps) wait_pieces<(kAhead - 1) * (XJ + YJ)>();
+            else wait_pieces<0>();
+        } else {
+            put(buf);
+        }
         __syncthreads();
-        if (s0 + KS < s1) {
-            fetch(s0 + KS, buf ^ 1);
-            sources(s0 + 2 * KS);
+        if (i + kAhead < steps) {
+            fetch(lr.s0 + (i + kAhead) * KS, buf + kAhead < kStages ? buf + kAhead : buf + kAhead - kStages);
+            sources(lr.s0 + (i + kAhead + 1) * KS);
         }
         const char* tx = lds + buf * kStage;
         const char* ty = tx + S::kABytes;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kFrags; ++j) {
             uint4 fx[2], fy[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -501,12 +545,17 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear_dw(const GradArgs a) {
                 fy[i] = YT::frag(ty, wo + 32 * i, j);
             }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int i = 0; i < 2; ++i)
+                if (live[i]) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) acc[i][h] = mma<T>(fx[i], fy[h], acc[i][h]);
-                if (with_db) sum[h] = mma<T>(ones<T>(), fy[h], sum[h]);
+                    for (int h = 0; h < 2; ++h) acc[i][h] = mma<T>(fy[h], fx[i], acc[i][h]);
+                }
+            if (with_db) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) sum[h] = mma<T>(fy[h], ones<T>(), sum[h]);
             }
         }
+        buf = buf + 1 < kStages ? buf + 1 : 0;
     }
 
     // a list of one chunk writes its gradient, a longer one a partial slot
@@ -517,23 +566,21 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear_dw(const GradArgs a) {
         dw = a.part + slot * ((int64_t)a.d_out * a.d_in + a.d_out);
         db = with_db ? dw + (int64_t)a.d_out * a.d_in : nullptr;
     }
-    // lane: output o = lane % 32, four consecutive inputs per register group
+    // lane: input i = lane % 32, so that a register's store covers 128 bytes of two rows; outputs
+    // 8 (r / 4) + 4 (lane / 32) + r % 4
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int o = o0 + wo + 32 * h + (lane & 31);
-        if (o >= a.d_out) continue;
-        if (with_db && lane < 32) db[o] = sum[h][0];
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int r = 0; r < 16; ++r) {
+            const int o = o0 + wo + 32 * h + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+            if (o >= a.d_out) continue;
+            if (with_db && (lane & 31) == 0) db[o] = sum[h][r];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int c = i0 + wi + 32 * i + 8 * q + 4 * (lane >> 5);
-                float v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = acc[i][h][4 * q + e];
-                store4<float, VEC>(dw + (int64_t)o * a.d_in, c, a.d_in, v);
+            for (int i = 0; i < 2; ++i) {
+                const int c = i0 + wi + 32 * i + (lane & 31);
+                if (c < a.d_in) dw[(int64_t)o * a.d_in + c] = acc[i][h][r];
             }
-    }
+        }
 }
 
 // The partial slots of the lists of several chunks, summed in order; zeros for

@@ -33,15 +33,16 @@ typedef short short4v __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) short4v lds_short4;
 typedef __attribute__((address_space(3))) char lds_char;
 
-constexpr int kStep = 64;      // bytes of the contraction a step
-constexpr int kFrags = kStep / 32;   // fragments of a step
-constexpr int kStages = 3;     // steps in LDS: one multiplied, the others on their way
-
-// Waves of a workgroup along the rows and along the columns of its tile.
-template <int WM, int WN> struct Shape {
+// A workgroup: its waves along the rows and along the columns of its tile, the
+// bytes of the contraction a step takes, the steps in LDS (one multiplied, the others on their way)
+// and the workgroups a compute unit is meant to hold.
+template <int WM_, int WN_, int STEP, int STAGES, int HELD> struct Shape {
+    static constexpr int WM = WM_, WN = WN_, kStep = STEP, kStages = STAGES, kHeld = HELD;
     static constexpr int kThreads = 64 * WM * WN, kM = 64 * WM, kN = 64 * WN;
+    static constexpr int kFrags = kStep / 32;   // fragments of a step
     static constexpr int kABytes = kM * kStep, kBBytes = kN * kStep;   // one operand, one step
     static constexpr int kStage = kABytes + kBBytes;
+    static constexpr int kWavesPerSimd = HELD * WM * WN / 4;
     static constexpr int kWaves = WM * WN;
     static constexpr int kAJ = kABytes / 1024 / kWaves, kBJ = kBBytes / 1024 / kWaves;   // wave loads a step
 };
@@ -56,6 +57,12 @@ __device__ __forceinline__ void fetch_piece(const void* g, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(g) : "memory", "m0");
 }
 template <int N> __device__ __forceinline__ void wait_pieces() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+// Its address in vector registers, so that a loop with waits in it does not load it again.
+__device__ __forceinline__ const char* zero_address() {
+    const char* p = (const char*)&zero_piece;
+    asm volatile("" : "+v"(p));
+    return p;
+}
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
     return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p);
 }
@@ -85,18 +92,32 @@ template <> __device__ __forceinline__ f32x16 mma<float>(const uint4& a, const u
     return __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.w), __uint_as_float(b.w), c, 0, 0, 0);
 }
 
-template <typename T> __device__ __forceinline__ uint4 ones();
-template <> __device__ __forceinline__ uint4 ones<float>() {
-    const uint32_t u = 0x3F800000u;
-    return make_uint4(u, u, u, u);
+// The same on 16 x 16 blocks: lane l gives row l % 16, quarter l / 16 of the
+// contraction (32 or 16), and holds column l % 16, rows 4 (l / 16) + r.
+template <typename T> __device__ __forceinline__ f32x4 mma16(const uint4& a, const uint4& b, f32x4 c);
+template <> __device__ __forceinline__ f32x4 mma16<_Float16>(const uint4& a, const uint4& b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
 }
-template <> __device__ __forceinline__ uint4 ones<bf16_t>() {
-    const uint32_t u = 0x3F803F80u;
-    return make_uint4(u, u, u, u);
+template <> __device__ __forceinline__ f32x4 mma16<bf16_t>(const uint4& a, const uint4& b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bfrag8, a), __builtin_bit_cast(bfrag8, b), c, 0, 0, 0);
 }
-template <> __device__ __forceinline__ uint4 ones<_Float16>() {
-    const uint32_t u = 0x3C003C00u;
-    return make_uint4(u, u, u, u);
+template <> __device__ __forceinline__ f32x4 mma16<float>(const uint4& a, const uint4& b, f32x4 c) {
+    c = mfma16x16x4(__uint_as_float(a.x), __uint_as_float(b.x), c);
+    c = mfma16x16x4(__uint_as_float(a.y), __uint_as_float(b.y), c);
+    c = mfma16x16x4(__uint_as_float(a.z), __uint_as_float(b.z), c);
+    return mfma16x16x4(__uint_as_float(a.w), __uint_as_float(b.w), c);
+}
+
+// A fragment of a 32 x 32 block has rows 0-15 in the even and rows 16-31 in the odd
+// groups of 16 lanes; taken as the second operand of a 16 x 16 product against
+// this first one (row 0: ones in the even groups, row 1: ones in the odd ones), row 0 and
+// row 1 of the product are the sums of the fragment's rows over the contraction.
+template <typename T> __device__ __forceinline__ uint4 row_sums() {
+    const int lane = threadIdx.x & 63;
+    T one[Vec16<T>::kElems];
+#pragma unroll
+    for (int i = 0; i < Vec16<T>::kElems; ++i) from_f32((lane & 15) == (lane >> 4 & 1) ? 1.0f : 0.0f, one + i);
+    return __builtin_bit_cast(uint4, one);
 }
 
 // 16 bytes of a row from element c on, of `width` elements, at any alignment of
@@ -146,7 +167,7 @@ template <typename T, bool VEC> __device__ __forceinline__ void store4(T* row, i
 
 // [row][kStep bytes]: pieces XOR-swizzled so that the 8 rows that one LDS cycle of
 // a fragment read touches lie in 8 different places of the 256 bytes of banks.
-struct RowTile {
+template <int kStep> struct RowTile {
     static constexpr int kPieces = kStep / 16, kRowsPerLoad = 64 / kPieces;
     __device__ __forceinline__ static int swz(int row) { return kPieces == 8 ? row & 7 : (row >> 2) & 3; }
     __device__ __forceinline__ static int at(int row, int piece) { return row * kStep + ((piece ^ swz(row)) << 4); }
@@ -158,7 +179,7 @@ struct RowTile {
 };
 
 // [contraction][N columns].
-template <typename T, int N> struct ColTile {
+template <typename T, int N, int kStep> struct ColTile {
     static constexpr int kRows = kStep / (int)sizeof(T);         // contraction elements of a step
     static constexpr int kPieces = N * (int)sizeof(T) / 16;      // 16-byte pieces of a row
     // Pairs of pieces (the 16 columns of a transposed read) move by a number
@@ -223,10 +244,11 @@ __device__ __forceinline__ int tile_of(int block, int tiles) {
 }
 
 // y = x W^T + b (BACK false) or dx = dy W (BACK true) on one tile.
-template <typename T, bool VEC, bool BACK, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 3) void k_linear(const LinArgs a) {
-    using S = Shape<WM, WN>;
-    using CT = ColTile<T, S::kN>;
+template <typename T, bool VEC, bool BACK, typename S>
+__global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear(const LinArgs a) {
+    constexpr int WM = S::WM, kStep = S::kStep, kStages = S::kStages, kFrags = S::kFrags;
+    using RT = RowTile<kStep>;
+    using CT = ColTile<T, S::kN, kStep>;
     constexpr int E = Vec16<T>::kElems, KS = kStep / (int)sizeof(T);   // elements of a piece, of a step
     constexpr int AJ = S::kAJ, BJ = S::kBJ, kStage = S::kStage;
     constexpr int kOut = S::kWaves * 32 * 64 * (int)sizeof(T);   // the epilogue's rows
@@ -243,9 +265,15 @@ __global__ __launch_bounds__(64 * WM * WN, 3) void k_linear(const LinArgs a) {
 
     // Wave load j covers the RA tile rows from RA (wave AJ + j) on; the piece that sits at
     // place p of a row is p ^ swz(row), the same for every j (RA rows are a whole period).
-    constexpr int PA = RowTile::kPieces, RA = RowTile::kRowsPerLoad;
-    const int ca = ((lane % PA) ^ RowTile::swz(lane / PA)) * E;
-    const T* pa[AJ];
+    constexpr int PA = RT::kPieces, RA = RT::kRowsPerLoad;
+    const int ca = ((lane % PA) ^ RT::swz(lane / PA)) * E;
+    // Each wave load has its own pointer, advanced by the step; where a lane has no row or
+    // column it stays on the zero piece.
+    const char* zero = zero_address();
+    const char *pa[AJ], *pb[BJ];
+    int64_t sa[AJ], sb[BJ];   // bytes a step
+    bool there_a[AJ], there_b[BJ];
+    int rb[BJ];               // BACK: contraction row within the step
     int e[AJ];
     if (a.gather) {
 #pragma unroll
@@ -255,49 +283,58 @@ __global__ __launch_bounds__(64 * WM * WN, 3) void k_linear(const LinArgs a) {
     for (int j = 0; j < AJ; ++j) {
         const int s = lr.s0 + RA * (wave * AJ + j) + lane / PA;
         const int row = a.gather ? source_row(e[j], a.magic, a.rows) : s;
-        pa[j] = s < lr.s1 && row >= 0 ? (const T*)a.a + (int64_t)row * a.lda : nullptr;
+        there_a[j] = s < lr.s1 && row >= 0;
+        pa[j] = there_a[j] ? (const char*)((const T*)a.a + (int64_t)row * a.lda + (VEC ? ca : 0)) : zero;
+        sa[j] = there_a[j] ? kStep : 0;
     }
-    const T* pb[BJ];   // FWD: weight rows; BACK: the first step's pieces
-    int rb[BJ];        // BACK: contraction row within the step
     constexpr int RI = 64 / CT::kPieces;   // BACK: tile rows of a wave load
-    int cb = ca;
 #pragma unroll
     for (int j = 0; j < BJ; ++j) {
         if constexpr (!BACK) {
             const int r = n0 + RA * (wave * BJ + j) + lane / PA;
-            pb[j] = r < nd ? w + (int64_t)r * kd : nullptr;
+            there_b[j] = r < nd;
+            pb[j] = there_b[j] ? (const char*)(w + (int64_t)r * kd + (VEC ? ca : 0)) : zero;
+            sb[j] = there_b[j] ? kStep : 0;
+            rb[j] = 0;
         } else {
             rb[j] = (wave * BJ + j) * RI + lane / CT::kPieces;
             const int c = n0 + ((lane % CT::kPieces) ^ CT::swz(rb[j])) * E;
-            pb[j] = c < nd ? w + c : nullptr;
+            there_b[j] = c < nd;
+            pb[j] = there_b[j] ? (const char*)(w + (int64_t)rb[j] * nd + (VEC ? c : 0)) : zero;
+            sb[j] = there_b[j] ? (int64_t)KS * nd * (int)sizeof(T) : 0;
         }
     }
     const uint32_t base = lds_address(lds);
     uint4 ra[VEC ? 1 : AJ], rbv[VEC ? 1 : BJ];
-    // the pieces of the step at k0: VEC into buffer `buf`, else into registers
+    // the pieces of the step at k0, the next one not yet fetched: VEC into buffer `buf`, else into registers
     auto fetch = [&](int k0, int buf) {
-        const uint32_t to = base + buf * kStage;
+        if constexpr (VEC) {
+            const uint32_t to = base + buf * kStage;
+            const bool whole = k0 + KS <= kd;
 #pragma unroll
-        for (int j = 0; j < AJ; ++j) {
-            if constexpr (VEC) {
-                const bool ok = pa[j] != nullptr && k0 + ca < kd;
-                fetch_piece(ok ? (const void*)(pa[j] + k0 + ca) : (const void*)&zero_piece, to + (wave * AJ + j) * 1024);
-            } else {
-                ra[j] = pa[j] != nullptr ? load_piece<T>(pa[j], k0 + ca, kd) : make_uint4(0, 0, 0, 0);
+            for (int j = 0; j < AJ; ++j) {
+                fetch_piece(whole || k0 + ca < kd ? pa[j] : zero, to + (wave * AJ + j) * 1024);
+                pa[j] += sa[j];
             }
-        }
 #pragma unroll
-        for (int j = 0; j < BJ; ++j) {
-            const int r = BACK ? k0 + rb[j] : 0;
-            if constexpr (VEC) {
-                const bool ok = pb[j] != nullptr && (BACK ? r < kd : k0 + cb < kd);
-                const T* p = BACK ? pb[j] + (int64_t)r * nd : pb[j] + k0 + cb;
-                fetch_piece(ok ? (const void*)p : (const void*)&zero_piece, to + S::kABytes + (wave * BJ + j) * 1024);
-            } else if constexpr (BACK) {
-                const int c = n0 + ((lane % CT::kPieces) ^ CT::swz(rb[j])) * E;
-                rbv[j] = r < kd ? load_piece<T>(w + (int64_t)r * nd, c, nd) : make_uint4(0, 0, 0, 0);
-            } else {
-                rbv[j] = pb[j] != nullptr ? load_piece<T>(pb[j], k0 + cb, kd) : make_uint4(0, 0, 0, 0);
+            for (int j = 0; j < BJ; ++j) {
+                fetch_piece(whole || k0 + (BACK ? rb[j] : ca) < kd ? pb[j] : zero, to + S::kABytes + (wave * BJ + j) * 1024);
+                pb[j] += sb[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < AJ; ++j)
+                ra[j] = there_a[j] ? load_piece<T>((const T*)pa[j], k0 + ca, kd) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < BJ; ++j) {
+                rbv[j] = make_uint4(0, 0, 0, 0);
+                if constexpr (BACK) {
+                    const int c = n0 + ((lane % CT::kPieces) ^ CT::swz(rb[j])) * E;
+                    if (there_b[j] && k0 + rb[j] < kd) rbv[j] = load_piece<T>((const T*)pb[j], c, nd);
+                    pb[j] += sb[j];
+                } else if (there_b[j]) {
+                    rbv[j] = load_piece<T>((const T*)pb[j], k0 + ca, kd);
+                }
             }
         }
     };
@@ -309,7 +346,8 @@ __global__ __launch_bounds__(64 * WM * WN, 3) void k_linear(const LinArgs a) {
         for (int j = 0; j < BJ; ++j) *(uint4*)(to + S::kABytes + (wave * BJ + j) * 1024) = rbv[j];
     };
 
-    const bool live[2] = {n0 + wn < nd, n0 + wn + 32 < nd};   // blocks of columns with outputs
+    // blocks of columns with outputs (VEC: not worth the branches, its loads bound narrow models)
+    const bool live[2] = {VEC || n0 + wn < nd, VEC || n0 + wn + 32 < nd};
     f32x16 acc[2][2] = {};
     if (!BACK && a.bias != nullptr) {   // sums start from the bias
         const float* bias = a.bias + (int64_t)lr.k * nd;
@@ -350,8 +388,8 @@ __global__ __launch_bounds__(64 * WM * WN, 3) void k_linear(const LinArgs a) {
             uint4 fa[2], fb[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                fa[i] = RowTile::frag(ta, wm + 32 * i, j);
-                fb[i] = BACK ? CT::frag(tb, wn + 32 * i, j) : RowTile::frag(tb, wn + 32 * i, j);
+                fa[i] = RT::frag(ta, wm + 32 * i, j);
+                fb[i] = BACK ? CT::frag(tb, wn + 32 * i, j) : RT::frag(tb, wn + 32 * i, j);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -419,6 +457,63 @@ __global__ __launch_bounds__(64 * WM * WN, 3) void k_linear(const LinArgs a) {
     }
 }
 
+// ---- few rows
+
+constexpr int kFewRows = 16, kFewOutputs = 16, kFewWaves = 4;
+
+// y = x W^T + b on 16 outputs of up to 16 rows of a list: nothing to share between
+// workgroups, so no LDS tiles.  The waves split the contraction, every lane streams its row of
+// W_k and of x into 16 x 16 products, and the four partial blocks are summed in order.
+template <typename T, bool VEC>
+__global__ __launch_bounds__(64 * kFewWaves) void k_linear_few(const LinArgs a) {
+    constexpr int E = Vec16<T>::kElems, KS = 4 * E;   // contraction of a product
+    constexpr int kAhead = 4;                         // products whose pieces are in flight
+    __shared__ f32x4 part[kFewWaves][64];
+    const int row_block = blockIdx.x / a.col_blocks, n0 = blockIdx.x % a.col_blocks * kFewOutputs;
+    const ListRows lr = find_rows(a.offsets, a.K, a.rows, row_block, kFewRows, a.by_slot);
+    if (lr.k < 0) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int s = lr.s0 + (lane & 15), o = n0 + (lane & 15);
+    int row = s < lr.s1 ? s : -1;
+    if (a.gather) {
+        const int e = a.entry[min(s, lr.s1 - 1)];
+        row = s < lr.s1 ? source_row(e, a.magic, a.rows) : -1;
+    }
+    const T* w = (const T*)a.w + ((int64_t)lr.k * a.d_out + min(o, a.d_out - 1)) * a.d_in;
+    const T* x = (const T*)a.a + (int64_t)max(row, 0) * a.lda;
+    const bool has_w = o < a.d_out, has_x = row >= 0;
+    f32x4 acc = {};
+    const int mine = (lane >> 4) * E;
+    auto piece = [&](const T* p, bool there, int k) {
+        if (!there || k >= a.d_in) return make_uint4(0, 0, 0, 0);
+        if constexpr (VEC) return *(const uint4*)(p + k);
+        else return load_piece<T>(p, k, a.d_in);
+    };
+    for (int k0 = wave * KS; k0 < a.d_in; k0 += kAhead * kFewWaves * KS) {
+        uint4 fw[kAhead], fx[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            fw[u] = piece(w, has_w, k0 + u * kFewWaves * KS + mine);
+            fx[u] = piece(x, has_x, k0 + u * kFewWaves * KS + mine);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) acc = mma16<T>(fw[u], fx[u], acc);
+    }
+    part[wave][lane] = acc;
+    __syncthreads();
+    if (wave != 0 || s >= lr.s1) return;
+    const int c = n0 + 4 * (lane >> 4);
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[e] = acc[e];
+#pragma unroll
+        for (int q = 1; q < kFewWaves; ++q) v[e] += part[q][lane][e];
+        if (a.bias != nullptr) v[e] += a.bias[(int64_t)lr.k * a.d_out + min(c + e, a.d_out - 1)];
+    }
+    store4<T, VEC>((T*)a.c + (int64_t)s * a.ldc, c, a.d_out, v);
+}
+
 // ---- gradient of the weights
 
 struct GradArgs {
@@ -445,21 +540,26 @@ struct GradArgs {
 __device__ __host__ __forceinline__ int64_t first_slot(int64_t a, int chunk) { return 2 * a / chunk; }
 
 // dW (and db) over one chunk of one list, one tile: 64 WM of d_in x 64 WN of d_out.
-template <typename T, bool VEC, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 3) void k_linear_dw(const GradArgs a) {
-    using S = Shape<WM, WN>;
-    using XT = ColTile<T, S::kM>;
-    using YT = ColTile<T, S::kN>;
+template <typename T, bool VEC, typename S>
+__global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear_dw(const GradArgs a) {
+    constexpr int WM = S::WM, kStages = S::kStages, kFrags = S::kFrags;
+    using XT = ColTile<T, S::kM, S::kStep>;
+    using YT = ColTile<T, S::kN, S::kStep>;
     constexpr int E = Vec16<T>::kElems, KS = XT::kRows;
     constexpr int XJ = S::kAJ, YJ = S::kBJ, kStage = S::kStage;
     constexpr int XR = 64 / XT::kPieces, YR = 64 / YT::kPieces;   // tile rows of a wave load
     __shared__ char lds[kStages * kStage] __attribute__((aligned(16)));
+    __shared__ int source[2 * S::kThreads];
     const int per_row = a.in_blocks * a.out_blocks;
-    const int tile = tile_of(blockIdx.x, a.row_blocks * per_row);
-    if (tile >= a.row_blocks * per_row) return;
-    const ListRows lr = find_rows(a.offsets, a.K, a.rows, tile / per_row, a.chunk, a.by_slot);
+    // The lists' lengths differ, so each XCD takes an eighth of the tiles of every chunk (a run of
+    // them, which shares rows of x and dy); with fewer than 8 tiles, every eighth tile.
+    const int per = (per_row + 7) >> 3, b = blockIdx.x;
+    const int block = per_row < 8 ? b / per_row : (b >> 3) / per;
+    const int tile = per_row < 8 ? b % per_row : (b & 7) * per + (b >> 3) % per;
+    if (block >= a.row_blocks || tile >= per_row) return;
+    const ListRows lr = find_rows(a.offsets, a.K, a.rows, block, a.chunk, a.by_slot);
     if (lr.k < 0) return;
-    const int i0 = tile % a.in_blocks * S::kM, o0 = tile % per_row / a.in_blocks * S::kN;
+    const int i0 = tile % a.in_blocks * S::kM, o0 = tile / a.in_blocks * S::kN;
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wi = wave % WM * 64, wo = wave / WM * 64;
     const int first = lr.first;
@@ -468,40 +568,54 @@ __global__ __launch_bounds__(64 * WM * WN, 3) void k_linear_dw(const GradArgs a)
 
     const uint32_t base = lds_address(lds);
     uint4 rx[VEC ? 1 : XJ], ry[VEC ? 1 : YJ];
-    int from[XJ];   // rows of x behind this lane's slots of a step, -1: none
-    auto sources = [&](int s0) {
-        int e[XJ];
-        if (a.gather) {
-#pragma unroll
-            for (int j = 0; j < XJ; ++j) e[j] = a.entry[min(s0 + (wave * XJ + j) * XR + lane / XT::kPieces, s1 - 1)];
-        }
-#pragma unroll
-        for (int j = 0; j < XJ; ++j) {
-            const int s = s0 + (wave * XJ + j) * XR + lane / XT::kPieces;
-            from[j] = s < s1 ? a.gather ? source_row(e[j], a.magic, a.rows) : s : -1;
-        }
+    // Rows of x behind the slots, one slot a thread and segment of kThreads slots, two segments in
+    // LDS: an entry loaded in every step would be waited for behind the pieces on their way.
+    constexpr int R = S::kThreads, SPR = R / KS;   // slots, steps of a segment
+    auto entry_of = [&](int seg) {
+        const int64_t s = lr.s0 + (int64_t)seg * R + t;
+        if (s >= s1) return -1;
+        return a.gather ? a.entry[s] : (int)s;
     };
+    auto keep = [&](int seg, int e) {
+        if (a.gather) e = source_row(e, a.magic, a.rows);
+        source[(seg & 1) * R + t] = e;
+    };
+    keep(0, entry_of(0));
+    __syncthreads();
+    const char* zero = zero_address();
+    int cx[XJ];           // column of this lane's piece of x
+    const char* py[YJ];   // dy, advanced by the step
+    int64_t sy[YJ];
+    int cy[YJ], rowy[YJ];
+#pragma unroll
+    for (int j = 0; j < XJ; ++j)
+        cx[j] = i0 + ((lane % XT::kPieces) ^ XT::swz((wave * XJ + j) * XR + lane / XT::kPieces)) * E;
+#pragma unroll
+    for (int j = 0; j < YJ; ++j) {
+        rowy[j] = lr.s0 + (wave * YJ + j) * YR + lane / YT::kPieces;
+        cy[j] = o0 + ((lane % YT::kPieces) ^ YT::swz((wave * YJ + j) * YR + lane / YT::kPieces)) * E;
+        const bool there = cy[j] < a.d_out;
+        py[j] = there ? (const char*)((const T*)a.dy + (int64_t)rowy[j] * a.ldy + (VEC ? cy[j] : 0)) : zero;
+        sy[j] = there ? (int64_t)KS * a.ldy * (int)sizeof(T) : 0;
+    }
+    // the step at slot s0, the next one not yet fetched; its rows of x are in from[]
     auto fetch = [&](int s0, int buf) {
         const uint32_t to = base + buf * kStage;
+        const bool whole = s0 + KS <= s1;
 #pragma unroll
         for (int j = 0; j < XJ; ++j) {
-            const int r = (wave * XJ + j) * XR + lane / XT::kPieces;
-            const int c = i0 + ((lane % XT::kPieces) ^ XT::swz(r)) * E;
-            const T* row = (const T*)a.x + (int64_t)from[j] * a.ldx;
-            if constexpr (VEC)
-                fetch_piece(from[j] >= 0 && c < a.d_in ? (const void*)(row + c) : (const void*)&zero_piece,
-                            to + (wave * XJ + j) * 1024);
-            else rx[j] = from[j] >= 0 ? load_piece<T>(row, c, a.d_in) : make_uint4(0, 0, 0, 0);
+            const int from = source[(s0 - lr.s0 + (wave * XJ + j) * XR + lane / XT::kPieces) & (2 * R - 1)];
+            const bool there = from >= 0 && cx[j] < a.d_in;
+            const char* row = (const char*)((const T*)a.x + (int64_t)from * a.ldx);
+            if constexpr (VEC) fetch_piece(there ? row + cx[j] * (int)sizeof(T) : zero, to + (wave * XJ + j) * 1024);
+            else rx[j] = there ? load_piece<T>((const T*)row, cx[j], a.d_in) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int j = 0; j < YJ; ++j) {
-            const int r = (wave * YJ + j) * YR + lane / YT::kPieces, s = s0 + r;
-            const int c = o0 + ((lane % YT::kPieces) ^ YT::swz(r)) * E;
-            const T* row = (const T*)a.dy + (int64_t)s * a.ldy;
-            if constexpr (VEC)
-                fetch_piece(s < s1 && c < a.d_out ? (const void*)(row + c) : (const void*)&zero_piece,
-                            to + S::kABytes + (wave * YJ + j) * 1024);
-            else ry[j] = s < s1 ? load_piece<T>(row, c, a.d_out) : make_uint4(0, 0, 0, 0);
+            const bool there = whole || s0 - lr.s0 + rowy[j] < s1;
+            if constexpr (VEC) fetch_piece(there ? py[j] : zero, to + S::kABytes + (wave * YJ + j) * 1024);
+            else ry[j] = there ? load_piece<T>((const T*)py[j], cy[j], a.d_out) : make_uint4(0, 0, 0, 0);
+            py[j] += sy[j];
         }
     };
     auto put = [&](int buf) {
@@ -512,16 +626,15 @@ __global__ __launch_bounds__(64 * WM * WN, 3) void k_linear_dw(const GradArgs a)
         for (int j = 0; j < YJ; ++j) *(uint4*)(to + S::kABytes + (wave * YJ + j) * 1024) = ry[j];
     };
 
-    const bool live[2] = {i0 + wi < a.d_in, i0 + wi + 32 < a.d_in};   // blocks with gradients
-    f32x16 acc[2][2] = {}, sum[2] = {};
+    const bool live[2] = {VEC || i0 + wi < a.d_in, VEC || i0 + wi + 32 < a.d_in};   // blocks with gradients
+    f32x16 acc[2][2] = {};
+    f32x4 sum[2] = {};
+    const uint4 ones = row_sums<T>();
     const int steps = (s1 - lr.s0 + KS - 1) / KS;
     constexpr int kAhead = VEC ? kStages - 1 : 1;
-    for (int i = 0; i < kAhead && i < steps; ++i) {
-        sources(lr.s0 + i * KS);
-        fetch(lr.s0 + i * KS, i);
-    }
-    sources(lr.s0 + kAhead * KS);
-    int buf = 0;
+    for (int i = 0; i < kAhead && i < steps; ++i) fetch(lr.s0 + i * KS, i);
+    int buf = 0, next = -1;   // next: the entry of this thread's slot in the segment after the one being fetched
+    static_assert(SPR - 3 >= kAhead && (R & (R - 1)) == 0, "a segment is loaded and kept while its forerunner is fetched");
     for (int i = 0; i < steps; ++i) {
         if constexpr (VEC) {
             if (i + kAhead - 1 < steps) wait_pieces<(kAhead - 1) * (XJ + YJ)>();
@@ -529,10 +642,13 @@ __global__ __launch_bounds__(64 * WM * WN, 3) void k_linear_dw(const GradArgs a)
         } else {
             put(buf);
         }
+        // the last step of a segment is about to be fetched: every wave is past the segment before it
+        const int f = i + kAhead;
+        if (f % SPR == SPR - 1) keep(f / SPR + 1, next);
         __syncthreads();
-        if (i + kAhead < steps) {
-            fetch(lr.s0 + (i + kAhead) * KS, buf + kAhead < kStages ? buf + kAhead : buf + kAhead - kStages);
-            sources(lr.s0 + (i + kAhead + 1) * KS);
+        if (f < steps) {
+            fetch(lr.s0 + f * KS, buf + kAhead < kStages ? buf + kAhead : buf + kAhead - kStages);
+            if (f % SPR == SPR - 3) next = entry_of(f / SPR + 1);
         }
         const char* tx = lds + buf * kStage;
         const char* ty = tx + S::kABytes;
@@ -552,7 +668,7 @@ __global__ __launch_bounds__(64 * WM * WN, 3) void k_linear_dw(const GradArgs a)
                 }
             if (with_db) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) sum[h] = mma<T>(fy[h], ones<T>(), sum[h]);
+                for (int h = 0; h < 2; ++h) sum[h] = mma16<T>(ones, fy[h], sum[h]);
             }
         }
         buf = buf + 1 < kStages ? buf + 1 : 0;
@@ -566,6 +682,13 @@ __global__ __launch_bounds__(64 * WM * WN, 3) void k_linear_dw(const GradArgs a)
         dw = a.part + slot * ((int64_t)a.d_out * a.d_in + a.d_out);
         db = with_db ? dw + (int64_t)a.d_out * a.d_in : nullptr;
     }
+    if (with_db && lane < 16) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                if (o0 + wo + 32 * h + 16 * r + lane < a.d_out) db[o0 + wo + 32 * h + 16 * r + lane] = sum[h][r];
+    }
     // lane: input i = lane % 32, so that a register's store covers 128 bytes of two rows; outputs
     // 8 (r / 4) + 4 (lane / 32) + r % 4
 #pragma unroll
@@ -574,7 +697,6 @@ __global__ __launch_bounds__(64 * WM * WN, 3) void k_linear_dw(const GradArgs a)
         for (int r = 0; r < 16; ++r) {
             const int o = o0 + wo + 32 * h + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
             if (o >= a.d_out) continue;
-            if (with_db && (lane & 31) == 0) db[o] = sum[h][r];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int c = i0 + wi + 32 * i + (lane & 31);
@@ -596,7 +718,15 @@ __global__ __launch_bounds__(256) void k_linear_dw_join(const GradArgs a) {
     const int64_t all = a.db != nullptr ? slot : wide;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
         float v = 0.0f;
-        for (int q = 0; q < chunks; ++q) v += part[q * slot + i];
+        int q = 0;
+        for (; q + 8 <= chunks; q += 8) {   // eight loads in flight, added in order
+            float p[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) p[u] = part[(q + u) * slot + i];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v += p[u];
+        }
+        for (; q < chunks; ++q) v += part[q * slot + i];
         if (i < wide) a.dw[k * wide + i] = v;
         else a.db[(int64_t)k * a.d_out + (i - wide)] = v;
     }
@@ -606,19 +736,21 @@ __global__ __launch_bounds__(256) void k_zero(float* p, int64_t n) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0.0f;
 }
 
-constexpr int kTile = 128;   // rows and columns of a tile: 2 x 2 waves
-
-// Rows of a list per workgroup of the weights' gradient: about 1024
-// workgroups over all tiles, at least 512 rows.
+// Rows of a list per workgroup of the weights' gradient: 1024 workgroups at most over all
+// tiles, and rows enough that writing and reading a partial slot (8 bytes a weight) costs no
+// more than reading the rows, as long as that leaves 256 workgroups.
 int chunk_rows(int64_t rows, const gmm_linear_desc* d) {
-    const int64_t tiles = ((d->d_in + kTile - 1) / kTile) * ((d->d_out + kTile - 1) / kTile);
-    int64_t chunk = (rows * tiles / 1024 + 511) / 512 * 512;
-    if (chunk < 512) chunk = 512;
-    const int64_t most = ((int64_t)1 << 30);
+    const int64_t tiles = ((d->d_in + 127) / 128) * ((d->d_out + 127) / 128);
+    const int64_t most_groups = rows * tiles / 1024, least_groups = rows * tiles / 256;
+    int64_t chunk = 8 * d->d_in * d->d_out / ((d->d_in + d->d_out) * elem_size(d->dtype));
+    if (chunk > least_groups) chunk = least_groups;
+    if (chunk < most_groups) chunk = most_groups;
+    chunk = (chunk / 128 + 1) * 128;
+    const int64_t most = (int64_t)1 << 30;
     return (int)(chunk > most ? most : chunk);
 }
 
-int blocks_of(int width) { return (width + kTile - 1) / kTile; }
+int blocks_of(int width, int tile) { return (width + tile - 1) / tile; }
 
 gmm_status check_desc(const gmm_linear_desc* d) {
     if (d == nullptr) return GMM_E_ARG;
@@ -635,40 +767,99 @@ gmm_status grid_of(int64_t tiles, int* grid) {
     return GMM_OK;
 }
 
-template <typename T, bool VEC, bool BACK> gmm_status launch_linear(const LinArgs& a, int64_t k, hipStream_t stream) {
+template <typename T, bool VEC, bool BACK, typename S>
+gmm_status launch_shape(const LinArgs& a, hipStream_t stream) {
     LinArgs b = a;
     int grid;
-    b.row_blocks = (int)row_blocks(a.rows, k, kTile, &b.by_slot);
-    b.col_blocks = blocks_of(BACK ? a.d_in : a.d_out);
+    b.row_blocks = (int)row_blocks(a.rows, a.K, S::kM, &b.by_slot);
+    b.col_blocks = blocks_of(BACK ? a.d_in : a.d_out, S::kN);
     const gmm_status st = grid_of((int64_t)b.row_blocks * b.col_blocks, &grid);
     if (st != GMM_OK) return st;
-    hipLaunchKernelGGL((k_linear<T, VEC, BACK, 2, 2>), dim3(grid), dim3(256), 0, stream, b);
+    hipLaunchKernelGGL((k_linear<T, VEC, BACK, S>), dim3(grid), dim3(S::kThreads), 0, stream, b);
     return launched();
 }
 
-template <bool BACK> gmm_status run_linear(const LinArgs& a, int64_t k, int dtype, bool vec, hipStream_t stream) {
+template <typename T, bool VEC> gmm_status launch_few(const LinArgs& a, hipStream_t stream) {
+    LinArgs b = a;
+    int grid;
+    b.row_blocks = (int)row_blocks(a.rows, a.K, kFewRows, &b.by_slot);
+    b.col_blocks = blocks_of(a.d_out, kFewOutputs);
+    const gmm_status st = grid_of((int64_t)b.row_blocks * b.col_blocks, &grid);
+    if (st != GMM_OK) return st;
+    hipLaunchKernelGGL((k_linear_few<T, VEC>), dim3(b.row_blocks * b.col_blocks), dim3(64 * kFewWaves), 0, stream, b);
+    return launched();
+}
+
+// Small: 128 x 128 tiles, several workgroups a compute unit, whose waits hide behind each
+// other.  Large: 256 x 256, half the operand traffic a product, one workgroup a compute unit.
+using Small = Shape<2, 2, 64, 2, 3>;
+using Large = Shape<4, 4, 128, 2, 1>;
+using LargeGrad = Shape<4, 4, 64, 3, 1>;
+
+// Large pays where its tiles go twice round the 256 compute units, a tile of a
+// short contraction counting for less (bf16, even lists, us, Small / Large: 64 lists of 512 rows,
+// 1024 -> 2048: 245 / 200; 256 of 1024, 256 -> 256: 88 / 75; 256 of 512, 256 -> 256:
+// 32 / 39; 8 of 512, 1024 -> 1024: 18 / 31).  fp32 is bound by its products.
+bool large_tiles(const LinArgs& a, int kd, int nd) {
+    const int64_t tiles = ((int64_t)a.rows + 255) / 256 * blocks_of(nd, 256);
+    return nd > 128 && tiles * (kd < 512 ? kd : 512) >= 512 * 512;
+}
+
+// Without tiles (k_linear_few) up to four rows a list or 128 rows in all (bf16, us,
+// few / Small: 1 list of 64 rows, 1024 -> 1024: 4.7 / 14.7; 16 lists of 8: 11 / 16, of 32: 22 / 16;
+// 256 lists of 4, 1024 -> 256: 28 / 30, of 16: 50 / 31).
+bool few_rows(const LinArgs& a) { return a.rows <= 4 * (int64_t)a.K || a.rows <= 128; }
+
+template <typename T, bool VEC, bool BACK> gmm_status launch_linear(const LinArgs& a, hipStream_t stream) {
+    if constexpr (!BACK)
+        if (few_rows(a)) return launch_few<T, VEC>(a, stream);
+    if constexpr (VEC && sizeof(T) == 2)
+        if (large_tiles(a, BACK ? a.d_out : a.d_in, BACK ? a.d_in : a.d_out))
+            return launch_shape<T, VEC, BACK, Large>(a, stream);
+    return launch_shape<T, VEC, BACK, Small>(a, stream);
+}
+
+template <bool BACK> gmm_status run_linear(const LinArgs& a, int dtype, bool vec, hipStream_t stream) {
     switch (dtype) {
         case GMM_F32:
-            return vec ? launch_linear<float, true, BACK>(a, k, stream) : launch_linear<float, false, BACK>(a, k, stream);
+            return vec ? launch_linear<float, true, BACK>(a, stream) : launch_linear<float, false, BACK>(a, stream);
         case GMM_BF16:
-            return vec ? launch_linear<bf16_t, true, BACK>(a, k, stream) : launch_linear<bf16_t, false, BACK>(a, k, stream);
+            return vec ? launch_linear<bf16_t, true, BACK>(a, stream) : launch_linear<bf16_t, false, BACK>(a, stream);
         default:
-            return vec ? launch_linear<_Float16, true, BACK>(a, k, stream)
-                       : launch_linear<_Float16, false, BACK>(a, k, stream);
+            return vec ? launch_linear<_Float16, true, BACK>(a, stream)
+                       : launch_linear<_Float16, false, BACK>(a, stream);
     }
 }
 
-template <typename T, bool VEC> gmm_status launch_dw(const GradArgs& a, hipStream_t stream) {
+template <typename T, bool VEC, typename S> gmm_status launch_dw_shape(const GradArgs& a, hipStream_t stream) {
     GradArgs b = a;
     int grid;
     b.row_blocks = (int)row_blocks(a.rows, a.K, a.chunk, &b.by_slot);
-    b.in_blocks = blocks_of(a.d_in), b.out_blocks = blocks_of(a.d_out);
-    const gmm_status st = grid_of((int64_t)b.row_blocks * b.in_blocks * b.out_blocks, &grid);
+    b.in_blocks = blocks_of(a.d_in, S::kM), b.out_blocks = blocks_of(a.d_out, S::kN);
+    const int64_t per = (int64_t)b.in_blocks * b.out_blocks;
+    const gmm_status st = grid_of(b.row_blocks * (per < 8 ? per : (per + 7) / 8 * 8), &grid);
     if (st != GMM_OK) return st;
-    hipLaunchKernelGGL((k_linear_dw<T, VEC, 2, 2>), dim3(grid), dim3(256), 0, stream, b);
+    hipLaunchKernelGGL((k_linear_dw<T, VEC, S>), dim3(grid), dim3(S::kThreads), 0, stream, b);
+    return launched();
+}
+
+// 256 x 256 tiles of the weights' gradient where lists average 512 rows and the
+// tiles fill the compute units (bf16, us, Small / LargeGrad: 64 lists of 512, 1024 x 2048: 298 / 255; 8 of 4096:
+// 205 / 154; 64 of 256, 512 x 512: 37 / 41; 256 of 2048, 128 x 256: 175 / 187).
+bool large_grad(const GradArgs& a) {
+    const int64_t tiles = (int64_t)blocks_of(a.d_in, 256) * blocks_of(a.d_out, 256);
+    return a.d_in >= 256 && a.d_out >= 256 && a.rows >= 512 * (int64_t)a.K && (a.rows / a.chunk + a.K) * tiles >= 256;
+}
+
+template <typename T, bool VEC> gmm_status launch_dw(const GradArgs& a, hipStream_t stream) {
+    gmm_status st;
+    if constexpr (VEC && sizeof(T) == 2)
+        st = large_grad(a) ? launch_dw_shape<T, VEC, LargeGrad>(a, stream) : launch_dw_shape<T, VEC, Small>(a, stream);
+    else st = launch_dw_shape<T, VEC, Small>(a, stream);
+    if (st != GMM_OK) return st;
     const int64_t wide = (int64_t)a.d_out * a.d_in;
-    const int64_t parts = (wide + a.d_out + 1023) / 1024;
-    hipLaunchKernelGGL(k_linear_dw_join, dim3(parts < 256 ? parts : 256, a.K), dim3(256), 0, stream, b);
+    const int64_t parts = (wide + a.d_out + 255) / 256;
+    hipLaunchKernelGGL(k_linear_dw_join, dim3(parts < 256 ? parts : 256, a.K), dim3(256), 0, stream, a);
     return launched();
 }
 
@@ -694,7 +885,7 @@ gmm_status gmm_linear(const gmm_routes* routes, const gmm_linear_desc* desc, con
     const int es = elem_size(desc->dtype);
     const bool vec = desc->d_in * es % 16 == 0 && desc->ldx * es % 16 == 0 && aligned16(x) && aligned16(w) &&
                      desc->d_out * es % 16 == 0 && desc->ldy * es % 16 == 0 && aligned16(y);
-    return run_linear<false>(a, routes->k, desc->dtype, vec, stream);
+    return run_linear<false>(a, desc->dtype, vec, stream);
 }
 
 gmm_status gmm_linear_backward_workspace_bytes(int64_t n, int32_t m, int32_t k, const gmm_linear_desc* desc,
@@ -736,7 +927,7 @@ gmm_status gmm_linear_backward(const gmm_routes* routes, const gmm_linear_desc* 
         LinArgs a = {routes->offsets, routes->entry, (int)rows, routes->k, magic_of(routes->m), false, false, dy,
                      desc->ldy, w, (int)desc->d_in, (int)desc->d_out, nullptr, dx, desc->lddx, 0, 0};
         const bool vec = wide && dy_vec && aligned16(w) && desc->lddx * es % 16 == 0 && aligned16(dx);
-        if ((st = run_linear<true>(a, routes->k, desc->dtype, vec, stream)) != GMM_OK) return st;
+        if ((st = run_linear<true>(a, desc->dtype, vec, stream)) != GMM_OK) return st;
     }
     if (dw == nullptr) return GMM_OK;
     if (rows == 0) {   // every list is empty

@@ -206,6 +206,32 @@ def test_linear(n, m, k, di, do, dt, pad, whole):
         R.close(R.f64(db[kk]), ref_b, (c + 1) * EPS * np.abs(dyk).sum(0), "db")
 
 
+@pytest.mark.parametrize("n,m,k,di,do,dt", [
+    (33_000, 2, 5, 520, 264, "bf16"), (70_000, 1, 3, 264, 776, "f16"), (20_000, 2, 40, 1032, 512, "bf16"),
+    (9_000, 2, 2, 512, 512, "f32"), (50_000, 2, 7, 77, 130, "f32"), (30_000, 1, 4, 300, 258, "bf16")])
+def test_linear_large(n, m, k, di, do, dt):
+    """Sizes whose tiles fill the GPU, lists of several chunks: whole numbers, exact sums, against
+    fp64 products on the GPU."""
+    rng = np.random.default_rng(di)
+    idx = R.assignment(n, m, k, rng, repeats=k < m)
+    idx[: n // 3, 0] = k - 1          # one long list
+    off, entry, slot = R.lists(idx, k)
+    r, t = routes_of(idx, k), R.DT[dt]
+    gen = torch.Generator(device="cuda").manual_seed(di)
+    whole = lambda *s: torch.randint(-2, 3, s, generator=gen, device="cuda")   # noqa: E731
+    x, w, dy, b = whole(n, di).to(t), whole(k, do, di).to(t), whole(n * m, do).to(t), whole(k, do).float()
+    y = experts.linear(x, w, b, r)
+    dx, dw, db = experts.linear_backward(dy, x, w, r)
+    point = torch.from_numpy(np.maximum(entry, 0) // m).cuda()
+    for kk in range(k):
+        s = slice(off[kk], off[kk + 1])
+        xk, dyk, wk = x[point[s]].double(), dy[s].double(), w[kk].double()
+        assert torch.equal(y[s], (xk @ wk.t().contiguous() + b[kk].double()).to(t)), (kk, "y")
+        assert torch.equal(dx[s], (dyk @ wk).to(t)), (kk, "dx")
+        assert torch.equal(dw[kk].double(), dyk.t().contiguous() @ xk), (kk, "dw")
+        assert torch.equal(db[kk].double(), dyk.sum(0)), (kk, "db")
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
 def test_linear_nonfinite_rows(dt):
     """A non-finite row touches its own outputs and its own list's gradient

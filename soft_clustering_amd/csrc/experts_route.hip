@@ -8,8 +8,10 @@
 // its key (one ballot per bit of the key).  Nothing depends on the order of
 // atomics: they only count.
 //
-// One workgroup does the whole sort of a small assignment in one launch;
-// larger ones take three: count per chunk, scan over chunks, place.
+// A workgroup of eight waves sorts a chunk of up to 8192 (16384) entries, its keys in
+// registers, in LDS first, so that entry[] leaves in runs.  A small assignment is one chunk and one launch;
+// larger ones take three: count per chunk, scan over chunks, place.  Reading idx twice and
+// writing entry and slot once bound it: 1e7 points in two of 256 lists, 240 MB once each.
 
 #include "experts_internal.h"
 
@@ -17,22 +19,13 @@ namespace gmm {
 
 namespace {
 
-constexpr int kSmallEntries = 8192;    // one workgroup up to here
-constexpr int kCounters = 16384;       // 16-bit counters in LDS: waves x lists
-constexpr int kMinChunk = 4096, kMaxChunk = 49152;   // entries per chunk; counters are 16 bits
-constexpr int kChunks = 1024;          // chunks aimed at
+constexpr int kWaves = 8, kThreads = 64 * kWaves;
 
-int waves_for(int k) {
-    int w = 16;
-    while (w > 1 && w * ((k + 1) & ~1) > kCounters) w >>= 1;
-    return w;
-}
+// Keys a lane holds, by the number of lists: the more lists, the longer the chunk whose
+// counters they share (hist is 4 K bytes a chunk).  Counters are 16 bits.
+constexpr int kKeysFew = 16, kKeysMany = 32, kManyLists = 1024;
 
-int64_t chunk_for(int64_t rows) {
-    int64_t c = (rows + kChunks - 1) / kChunks;
-    c = (c + kMinChunk - 1) / kMinChunk * kMinChunk;
-    return c > kMaxChunk ? kMaxChunk : c;
-}
+int64_t chunk_for(int k) { return (int64_t)kThreads * (k > kManyLists ? kKeysMany : kKeysFew); }
 
 __device__ __forceinline__ bool in_lists(int key, int K) { return (unsigned)key < (unsigned)K; }
 
@@ -78,150 +71,153 @@ __device__ int scan_keys(int* a, int K, int* scratch) {
     return total;
 }
 
-// Entries [c0, c1) of one workgroup: per-wave counts of its keys into cnt
-// [waves][kp] (16 bits each).
-__device__ __forceinline__ void count_waves(const int32_t* __restrict__ idx, int64_t c0, int64_t c1,
-                                            int64_t run, int K, int kp, uint32_t* cnt) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t a = c0 + wave * run, b = min(a + run, c1);
-    for (int64_t e = a + lane; e < b; e += 64) {
-        const int key = idx[e];
-        if (in_lists(key, K)) {
-            const int at = wave * kp + key;
-            atomicAdd(&cnt[at >> 1], 1u << (16 * (at & 1)));
-        }
-    }
-}
-
-// Turns the waves' counts into the waves' offsets within the workgroup, per
-// key; the workgroup's count goes to total[key] when it is asked for.
-__device__ __forceinline__ void prefix_waves(uint16_t* cnt, int waves, int K, int kp, int* total) {
-    for (int key = threadIdx.x; key < K; key += blockDim.x) {
-        int run = 0;
-        for (int w = 0; w < waves; ++w) {
-            const int c = cnt[w * kp + key];
-            cnt[w * kp + key] = (uint16_t)run;
-            run += c;
-        }
-        if (total != nullptr) total[key] = run;
-    }
-}
-
-__device__ __forceinline__ void place(const int32_t* __restrict__ idx, int64_t c0, int64_t c1, int64_t run,
-                                      int K, int kp, int bits, uint16_t* cnt, const int* base,
-                                      int32_t* __restrict__ entry, int32_t* __restrict__ slot) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t a = c0 + wave * run, b = min(a + run, c1);
-    for (int64_t e0 = a; e0 < b; e0 += 64) {
-        const int64_t e = e0 + lane;
-        const bool there = e < b;
-        const int key = there ? idx[e] : -1;
-        const bool valid = in_lists(key, K);
-        const uint64_t same = same_key(key, valid, bits);
-        const int rank = __popcll(same & ((1ull << lane) - 1));
-        int pos = -1;
-        if (valid) pos = base[key] + cnt[wave * kp + key] + rank;
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        if (valid && rank == 0) cnt[wave * kp + key] += (uint16_t)__popcll(same);
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        if (valid) entry[pos] = (int32_t)e;
-        if (there) slot[e] = pos;
-    }
-}
-
-// The whole sort in one workgroup.
-__global__ __launch_bounds__(1024) void k_route_small(const int32_t* __restrict__ idx, int rows, int K, int kp,
-                                                      int bits, int32_t* __restrict__ offsets,
-                                                      int32_t* __restrict__ entry, int32_t* __restrict__ slot) {
-    __shared__ uint32_t cnt[kCounters / 2];
-    __shared__ int base[GMM_MAX_LISTS];
-    __shared__ int scratch[16];
-    const int t = threadIdx.x, nt = blockDim.x, waves = nt / 64;
-    for (int i = t; i < waves * kp / 2; i += nt) cnt[i] = 0;
-    __syncthreads();
-    const int64_t run = ((rows + waves - 1) / waves + 63) / 64 * 64;
-    count_waves(idx, 0, rows, run, K, kp, cnt);
-    __syncthreads();
-    prefix_waves((uint16_t*)cnt, waves, K, kp, base);
-    __syncthreads();
-    const int total = scan_keys(base, K, scratch);
-    for (int i = t; i < K; i += nt) offsets[i] = base[i];
-    if (t == 0) offsets[K] = total;
-    place(idx, 0, rows, run, K, kp, bits, (uint16_t*)cnt, base, entry, slot);
-    for (int i = total + t; i < rows; i += nt) entry[i] = -1;
-}
-
-// Counts of every key in every chunk: hist [chunks][K].
+// Counts of every key in every chunk: hist [K][stride], a key's chunks side by
+// side, so that the scan reads and writes whole lines.
 __global__ __launch_bounds__(1024) void k_route_count(const int32_t* __restrict__ idx, int64_t rows,
-                                                      int64_t chunk, int K, int* __restrict__ hist) {
+                                                      int64_t chunk, int K, int stride, int* __restrict__ hist) {
     __shared__ int h[GMM_MAX_LISTS];
     const int t = threadIdx.x, nt = blockDim.x;
     for (int i = t; i < K; i += nt) h[i] = 0;
     __syncthreads();
     const int64_t c0 = blockIdx.x * chunk, c1 = min(c0 + chunk, rows);
-    for (int64_t e = c0 + t; e < c1; e += nt) {
-        const int key = idx[e];
-        if (in_lists(key, K)) atomicAdd(&h[key], 1);
+    for (int64_t e = c0 + t; e < c1; e += 8 * nt) {   // eight loads in flight
+        int key[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) key[u] = e + u * nt < c1 ? idx[e + u * nt] : -1;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (in_lists(key[u], K)) atomicAdd(&h[key[u]], 1);
     }
     __syncthreads();
-    for (int i = t; i < K; i += nt) hist[(int64_t)blockIdx.x * K + i] = h[i];
+    for (int i = t; i < K; i += nt) hist[(int64_t)i * stride + blockIdx.x] = h[i];
 }
 
-// hist -> exclusive sums over the chunks, per key; total[key].  64 keys a
-// workgroup, 16 waves on a part of the chunks each.
-__global__ __launch_bounds__(1024) void k_route_scan(int* __restrict__ hist, int chunks, int K,
-                                                     int* __restrict__ total) {
-    __shared__ int part[16][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int key = blockIdx.x * 64 + lane;
-    const bool there = key < K;
-    const int per = (chunks + 15) / 16, lo = min(wave * per, chunks), hi = min(lo + per, chunks);
-    int sum = 0;
-    for (int c = lo; c < hi; ++c) sum += there ? hist[(int64_t)c * K + key] : 0;
-    part[wave][lane] = sum;
-    __syncthreads();
-    int run = 0, all = 0;
-    for (int w = 0; w < 16; ++w) {
-        if (w < wave) run += part[w][lane];
-        all += part[w][lane];
+// hist -> exclusive sums over the chunks; total[key].  One workgroup a key.
+__global__ __launch_bounds__(256) void k_route_scan(int* __restrict__ hist, int chunks, int stride,
+                                                    int* __restrict__ total) {
+    constexpr int U = 8;
+    __shared__ int part[2][4];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    int* row = hist + (int64_t)blockIdx.x * stride;
+    int before = 0;   // the strips so far
+    for (int c0 = 0, turn = 0; c0 < chunks; c0 += 256 * U, turn ^= 1) {
+        int v[U], sum = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + t * U + u;
+            v[u] = c < chunks ? row[c] : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) sum += v[u];
+        int upto = sum;
+        for (int o = 1; o < 64; o <<= 1) {
+            const int w = __shfl_up(upto, o);
+            if (lane >= o) upto += w;
+        }
+        if (lane == 63) part[turn][wave] = upto;
+        __syncthreads();
+        int run = before + upto - sum;
+        for (int w = 0; w < 4; ++w) {
+            if (w < wave) run += part[turn][w];
+            before += part[turn][w];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + t * U + u;
+            if (c < chunks) row[c] = run;
+            run += v[u];
+        }
     }
-    if (!there) return;
-    if (wave == 0) total[key] = all;
-    for (int c = lo; c < hi; ++c) {
-        const int v = hist[(int64_t)c * K + key];
-        hist[(int64_t)c * K + key] = run;
-        run += v;
-    }
+    if (t == 0) total[blockIdx.x] = before;
 }
 
-__global__ __launch_bounds__(1024) void k_route_place(const int32_t* __restrict__ idx, int64_t rows, int64_t chunk,
-                                                      int K, int kp, int bits, const int* __restrict__ hist,
-                                                      const int* __restrict__ total, int32_t* __restrict__ offsets,
-                                                      int32_t* __restrict__ entry, int32_t* __restrict__ slot) {
-    __shared__ uint32_t cnt[kCounters / 2];
-    __shared__ int base[GMM_MAX_LISTS];
-    __shared__ int scratch[16];
-    const int t = threadIdx.x, nt = blockDim.x, waves = nt / 64;
-    for (int i = t; i < waves * kp / 2; i += nt) cnt[i] = 0;
-    for (int i = t; i < K; i += nt) base[i] = total[i];
+// One chunk: hist and total from the kernels above, or null for an assignment of one chunk.
+template <int KEYS, int KMAX>
+__global__ __launch_bounds__(kThreads) void k_route_place(const int32_t* __restrict__ idx, int64_t rows, int K,
+                                                          int bits, int stride, const int* __restrict__ hist,
+                                                          const int* __restrict__ total, int32_t* __restrict__ offsets,
+                                                          int32_t* __restrict__ entry, int32_t* __restrict__ slot) {
+    constexpr int kChunk = kThreads * KEYS;
+    __shared__ uint32_t cnt32[kWaves * KMAX / 2];   // [wave][key], 16 bits each
+    __shared__ int to[KMAX];                        // global minus local position of a key's entries
+    __shared__ uint16_t sorted[kChunk] __attribute__((aligned(4))), key_of[kChunk];
+    __shared__ int scratch[kWaves];
+    static_assert(sizeof(int) * KMAX <= sizeof(sorted), "local");
+    int* local = (int*)sorted;   // the chunk's counts, then their exclusive sums; before the keys are placed
+    uint16_t* cnt = (uint16_t*)cnt32;
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int64_t c0 = (int64_t)blockIdx.x * kChunk;
+    const int here = (int)min((int64_t)kChunk, rows - c0);
+    const int run = ((here + kWaves - 1) / kWaves + 63) / 64 * 64;   // entries of a wave
+    const int a = wave * run, b = min(a + run, here);
+
+    int key[KEYS];
+#pragma unroll
+    for (int g = 0; g < KEYS; ++g) {
+        const int e = a + 64 * g + lane;
+        key[g] = 64 * g < run && e < b ? idx[c0 + e] : -1;
+    }
+    for (int i = t; i < kWaves * KMAX / 2; i += kThreads) cnt32[i] = 0;
+    for (int i = t; i < K; i += kThreads) to[i] = total != nullptr ? total[i] : 0;
     __syncthreads();
-    const int64_t c0 = blockIdx.x * chunk, c1 = min(c0 + chunk, rows);
-    const int64_t run = ((c1 - c0 + waves - 1) / waves + 63) / 64 * 64;
-    count_waves(idx, c0, c1, run, K, kp, cnt);
-    const int all = scan_keys(base, K, scratch);
+#pragma unroll
+    for (int g = 0; g < KEYS; ++g)
+        if (in_lists(key[g], K)) {
+            const int at = wave * KMAX + key[g];
+            atomicAdd(&cnt32[at >> 1], 1u << (16 * (at & 1)));
+        }
+    int all = 0;
+    if (total != nullptr) all = scan_keys(to, K, scratch);   // the lists' first slots
+    __syncthreads();
+    for (int i = t; i < K; i += kThreads) {
+        int n = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) n += cnt[w * KMAX + i];
+        local[i] = n;
+    }
+    __syncthreads();
+    const int listed = scan_keys(local, K, scratch);
+    if (total == nullptr) all = listed;
     if (blockIdx.x == 0) {
-        for (int i = t; i < K; i += nt) offsets[i] = base[i];
+        for (int i = t; i < K; i += kThreads) offsets[i] = total != nullptr ? to[i] : local[i];
         if (t == 0) offsets[K] = all;
         __syncthreads();
     }
-    for (int i = t; i < K; i += nt) base[i] += hist[(int64_t)blockIdx.x * K + i];
+    for (int i = t; i < K; i += kThreads) {
+        // the waves' counts become their first local positions
+        int n = local[i];
+        to[i] = total != nullptr ? to[i] + hist[(int64_t)i * stride + blockIdx.x] - n : 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const int c = cnt[w * KMAX + i];
+            cnt[w * KMAX + i] = (uint16_t)n;
+            n += c;
+        }
+    }
     __syncthreads();
-    prefix_waves((uint16_t*)cnt, waves, K, kp, nullptr);
+#pragma unroll
+    for (int g = 0; g < KEYS; ++g) {
+        if (64 * g >= run) continue;
+        const int e = a + 64 * g + lane;
+        const bool valid = in_lists(key[g], K);
+        const uint64_t same = same_key(key[g], valid, bits);
+        const int rank = __popcll(same & ((1ull << lane) - 1));
+        int pos = -1;
+        if (valid) pos = cnt[wave * KMAX + key[g]] + rank;
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (valid && rank == 0) cnt[wave * KMAX + key[g]] = (uint16_t)(pos + __popcll(same));
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (valid) {
+            sorted[pos] = (uint16_t)e;
+            key_of[pos] = (uint16_t)key[g];
+        }
+        if (e < b) slot[c0 + e] = valid ? to[key[g]] + pos : -1;
+    }
     __syncthreads();
-    place(idx, c0, c1, run, K, kp, bits, (uint16_t*)cnt, base, entry, slot);
-    for (int64_t i = all + (int64_t)blockIdx.x * nt + t; i < rows; i += (int64_t)gridDim.x * nt) entry[i] = -1;
+    for (int i = t; i < listed; i += kThreads) entry[to[key_of[i]] + i] = (int32_t)(c0 + sorted[i]);
+    for (int64_t i = all + (int64_t)blockIdx.x * kThreads + t; i < rows; i += (int64_t)gridDim.x * kThreads) entry[i] = -1;
 }
 
 __global__ void k_route_empty(int K, int32_t* offsets) {
@@ -263,8 +259,9 @@ gmm_status gmm_route_workspace_bytes(int64_t n, int32_t m, int32_t k, size_t* by
     if (st != GMM_OK) return st;
     const int64_t rows = n * m;
     *bytes = 0;
-    if (rows > kSmallEntries) {
-        const int64_t chunk = chunk_for(rows), chunks = (rows + chunk - 1) / chunk;
+    const int64_t chunk = chunk_for(k);
+    if (rows > chunk) {
+        const int64_t chunks = (rows + chunk - 1) / chunk;
         *bytes = sizeof(int) * (size_t)(chunks + 1) * k;
     }
     return GMM_OK;
@@ -285,22 +282,24 @@ gmm_status gmm_route(int64_t n, int32_t m, int32_t k, const int32_t* idx, void* 
         hipLaunchKernelGGL(k_route_empty, dim3(1), dim3(256), 0, stream, k, offsets);
         return launched();
     }
-    const int kp = (k + 1) & ~1, waves = waves_for(k);
     int bits = 0;
     while ((1 << bits) < k) ++bits;
-    if (need == 0) {
-        hipLaunchKernelGGL(k_route_small, dim3(1), dim3(64 * waves), 0, stream, idx, (int)rows, k, kp, bits, offsets,
-                           entry, slot);
-        return launched();
-    }
-    const int64_t chunk = chunk_for(rows);
+    const int64_t chunk = chunk_for(k);
     const int chunks = (int)((rows + chunk - 1) / chunk);
-    int* hist = (int*)ws;
-    int* total = hist + (int64_t)chunks * k;
-    hipLaunchKernelGGL(k_route_count, dim3(chunks), dim3(1024), 0, stream, idx, rows, chunk, k, hist);
-    hipLaunchKernelGGL(k_route_scan, dim3((k + 63) / 64), dim3(1024), 0, stream, hist, chunks, k, total);
-    hipLaunchKernelGGL(k_route_place, dim3(chunks), dim3(64 * waves), 0, stream, idx, rows, chunk, k, kp, bits, hist,
-                       total, offsets, entry, slot);
+    int *hist = nullptr, *total = nullptr;
+    if (need > 0) {
+        hist = (int*)ws;
+        total = hist + (int64_t)chunks * k;
+        hipLaunchKernelGGL(k_route_count, dim3(chunks), dim3(1024), 0, stream, idx, rows, chunk, k, chunks, hist);
+        hipLaunchKernelGGL(k_route_scan, dim3(k), dim3(256), 0, stream, hist, chunks, chunks, total);
+    }
+    auto place = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(chunks), dim3(kThreads), 0, stream, idx, rows, k, bits, chunks, (const int*)hist,
+                           (const int*)total, offsets, entry, slot);
+    };
+    if (k <= 256) place(k_route_place<kKeysFew, 256>);
+    else if (k <= kManyLists) place(k_route_place<kKeysFew, kManyLists>);
+    else place(k_route_place<kKeysMany, GMM_MAX_LISTS>);
     return launched();
 }
 

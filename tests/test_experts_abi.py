@@ -52,13 +52,13 @@ def test_route_refusals():
         assert LIB.gmm_route(10, 2, 3, args[0], None, 0, *args[1:], None) == ARG
 
 
-def test_route_workspace_does_not_grow_with_points_times_lists():
-    """The counters stay near 1024 chunks x K whatever the number of points, until the chunks
-    reach their largest size; never the N x K matrix."""
-    size = lambda n: (LIB.gmm_route_workspace_bytes(n, 1, 4096, ctypes.byref(b)), b.value)[1]   # noqa: E731
+def test_route_workspace_far_below_points_times_lists():
+    """One counter a list for every 8192 entries (16384 with more than 1024 lists); never the
+    N x K matrix."""
     b = ctypes.c_size_t(0)
-    assert size(4_000_000) <= 1025 * 4096 * 4 and size(50_000_000) <= 1025 * 4096 * 4
-    assert size(1 << 30) <= (1 << 30) // 40_000 * 4096 * 4
+    for n, m, k in [(10 ** 7, 2, 256), (10 ** 8, 1, 4096), (1 << 30, 1, 4096), (10 ** 6, 16, 1024)]:
+        assert LIB.gmm_route_workspace_bytes(n, m, k, ctypes.byref(b)) == OK
+        assert b.value <= (n * m / 8192 + 2) * k * 4
 
 
 def test_rows_refusals():

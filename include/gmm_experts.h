@@ -144,9 +144,10 @@ gmm_status gmm_quantize4(int64_t rows, int64_t d_in, int32_t group, int32_t dtyp
 /* The single-point form, straight from the assignment: out[p] = sum over the
  * columns i with 0 <= idx[p * m + i] < k, in order, of gamma[p * m + i] * (W_k x[p] + b_k),
  * k = idx[p * m + i], W_k = (code - 8) * scale; zero for a point in no list.  For a few points:
- * every point reads its components' weights.  codes [k * d_out rows] and scales as
+ * every 16 of them read the weights of the components they list once.  codes [k * d_out rows] and scales as
  * gmm_quantize4 writes them, bias fp32 [k, d_out] or NULL; x [n, d_in] (stride ldx) and out
- * [n, d_out] (stride ldo) in dtype.  n <= GMM_LINEAR4_MAX_N. */
+ * [n, d_out] (stride ldo) in dtype.  n <= GMM_LINEAR4_MAX_N.  An infinity in x[p] makes the
+ * outputs of point p NaN or infinite. */
 #define GMM_LINEAR4_MAX_N 1024
 gmm_status gmm_linear4(int64_t n, int32_t m, int32_t k, int64_t d_in, int64_t d_out, int32_t group,
                        int32_t dtype, const void* x, int64_t ldx, const int32_t* idx, const float* gamma,

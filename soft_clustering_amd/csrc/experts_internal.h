@@ -23,6 +23,78 @@ template <typename T> __device__ __forceinline__ uint4 pack16(const float* v) {
     return __builtin_bit_cast(uint4, t);
 }
 
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bfrag8 __attribute__((ext_vector_type(8)));
+
+// c += A . B on 16 x 16 blocks: lane l gives row l % 16 of A and column l % 16 of B, quarter
+// l / 16 of the contraction (32 elements, fp32: 16), and holds column l % 16, rows 4 (l / 16) + r.
+template <typename T> __device__ __forceinline__ f32x4 mma16(const uint4& a, const uint4& b, f32x4 c);
+template <> __device__ __forceinline__ f32x4 mma16<_Float16>(const uint4& a, const uint4& b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
+}
+template <> __device__ __forceinline__ f32x4 mma16<bf16_t>(const uint4& a, const uint4& b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bfrag8, a), __builtin_bit_cast(bfrag8, b), c, 0, 0, 0);
+}
+template <> __device__ __forceinline__ f32x4 mma16<float>(const uint4& a, const uint4& b, f32x4 c) {
+    c = mfma16x16x4(__uint_as_float(a.x), __uint_as_float(b.x), c);
+    c = mfma16x16x4(__uint_as_float(a.y), __uint_as_float(b.y), c);
+    c = mfma16x16x4(__uint_as_float(a.z), __uint_as_float(b.z), c);
+    return mfma16x16x4(__uint_as_float(a.w), __uint_as_float(b.w), c);
+}
+
+// 16 bytes of a row from byte c on, of `width` >= 16 bytes, at any alignment; zero
+// beyond the row.  The last, shorter piece of a row is cut out of the row's last 16 bytes.
+__device__ __forceinline__ uint4 load_bytes(const char* row, int64_t c, int64_t width) {
+    if (c >= width) return make_uint4(0, 0, 0, 0);
+    const int64_t from = min(c, width - 16);
+    uint64_t v[2];
+    __builtin_memcpy(v, row + from, 16);
+    const int drop = 8 * (int)(c - from);   // bits before c
+    if (drop != 0) {
+        const bool far = drop >= 64;
+        const int by = drop & 63;
+        const uint64_t lo = far ? v[1] : v[0], hi = far ? 0 : v[1];
+        v[0] = (lo >> by) | (by ? hi << (64 - by) : 0);
+        v[1] = hi >> by;
+    }
+    return make_uint4((uint32_t)v[0], (uint32_t)(v[0] >> 32), (uint32_t)v[1], (uint32_t)(v[1] >> 32));
+}
+
+// 16 bytes of a row from element c on, of `width` elements, at any alignment of the elements; zero
+// beyond the row.
+template <typename T> __device__ __forceinline__ uint4 load_piece(const T* row, int c, int width) {
+    constexpr int E = Vec16<T>::kElems, S = (int)sizeof(T);
+    if (width >= E) return load_bytes((const char*)row, (int64_t)c * S, (int64_t)width * S);
+    T t[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        if (c + i < width) t[i] = row[c + i];
+        else from_f32(0.0f, t + i);
+    }
+    return __builtin_bit_cast(uint4, t);
+}
+
+static __device__ __constant__ uint4 zero_piece = {0, 0, 0, 0};
+
+// 16 bytes from each lane's address to LDS bytes lds + 16 lane, asynchronously: the wave that
+// issued it waits with wait_pieces() before the barrier that hands the tile over.  Written as asm
+// because the compiler, which tracks the builtin form as an LDS store, would wait
+// for the pieces of the next step before it reads those of this one.
+__device__ __forceinline__ void fetch_piece(const void* g, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(g) : "memory", "m0");
+}
+template <int N> __device__ __forceinline__ void wait_pieces() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+// Its address in vector registers, so that a loop with waits in it does not load it again.
+__device__ __forceinline__ const char* zero_address() {
+    const char* p = (const char*)&zero_piece;
+    asm volatile("" : "+v"(p));
+    return p;
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p);
+}
+
+
 // Workgroup -> rows of one list.  Row block `t` of a launch is either block
 // (t - t0_k) of the list k with the largest t0_k = offsets[k] / BM + k not
 // above t (a list of c rows spans at most the ceil(c / BM) blocks up to

@@ -27,8 +27,6 @@ namespace gmm {
 namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef _Float16 half8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bfrag8 __attribute__((ext_vector_type(8)));
 typedef short short4v __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) short4v lds_short4;
 typedef __attribute__((address_space(3))) char lds_char;
@@ -46,26 +44,6 @@ template <int WM_, int WN_, int STEP, int STAGES, int HELD> struct Shape {
     static constexpr int kWaves = WM * WN;
     static constexpr int kAJ = kABytes / 1024 / kWaves, kBJ = kBBytes / 1024 / kWaves;   // wave loads a step
 };
-
-__device__ __constant__ uint4 zero_piece = {0, 0, 0, 0};
-
-// 16 bytes from each lane's address to LDS bytes lds + 16 lane, asynchronously: the wave that
-// issued it waits with wait_pieces() before the barrier that hands the tile over.  Written as asm
-// because the compiler, which tracks the builtin form as an LDS store, would wait
-// for the pieces of the next step before it reads those of this one.
-__device__ __forceinline__ void fetch_piece(const void* g, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(g) : "memory", "m0");
-}
-template <int N> __device__ __forceinline__ void wait_pieces() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
-// Its address in vector registers, so that a loop with waits in it does not load it again.
-__device__ __forceinline__ const char* zero_address() {
-    const char* p = (const char*)&zero_piece;
-    asm volatile("" : "+v"(p));
-    return p;
-}
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p);
-}
 
 // e / m for 0 <= e < 2^30, 1 <= m <= 16, magic = 2^34 / m + 1: the excess of
 // magic is at most 1, so e magic / 2^34 exceeds e / m by less than 1 / 16, and
@@ -92,22 +70,6 @@ template <> __device__ __forceinline__ f32x16 mma<float>(const uint4& a, const u
     return __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.w), __uint_as_float(b.w), c, 0, 0, 0);
 }
 
-// The same on 16 x 16 blocks: lane l gives row l % 16, quarter l / 16 of the
-// contraction (32 or 16), and holds column l % 16, rows 4 (l / 16) + r.
-template <typename T> __device__ __forceinline__ f32x4 mma16(const uint4& a, const uint4& b, f32x4 c);
-template <> __device__ __forceinline__ f32x4 mma16<_Float16>(const uint4& a, const uint4& b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
-}
-template <> __device__ __forceinline__ f32x4 mma16<bf16_t>(const uint4& a, const uint4& b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bfrag8, a), __builtin_bit_cast(bfrag8, b), c, 0, 0, 0);
-}
-template <> __device__ __forceinline__ f32x4 mma16<float>(const uint4& a, const uint4& b, f32x4 c) {
-    c = mfma16x16x4(__uint_as_float(a.x), __uint_as_float(b.x), c);
-    c = mfma16x16x4(__uint_as_float(a.y), __uint_as_float(b.y), c);
-    c = mfma16x16x4(__uint_as_float(a.z), __uint_as_float(b.z), c);
-    return mfma16x16x4(__uint_as_float(a.w), __uint_as_float(b.w), c);
-}
-
 // A fragment of a 32 x 32 block has rows 0-15 in the even and rows 16-31 in the odd
 // groups of 16 lanes; taken as the second operand of a 16 x 16 product against
 // this first one (row 0: ones in the even groups, row 1: ones in the odd ones), row 0 and
@@ -118,35 +80,6 @@ template <typename T> __device__ __forceinline__ uint4 row_sums() {
 #pragma unroll
     for (int i = 0; i < Vec16<T>::kElems; ++i) from_f32((lane & 15) == (lane >> 4 & 1) ? 1.0f : 0.0f, one + i);
     return __builtin_bit_cast(uint4, one);
-}
-
-// 16 bytes of a row from element c on, of `width` elements, at any alignment of
-// the elements; zero beyond the row.  The last, shorter piece of a row is cut out of
-// the row's last 16 bytes.
-template <typename T> __device__ __forceinline__ uint4 load_piece(const T* row, int c, int width) {
-    constexpr int E = Vec16<T>::kElems;
-    if (c >= width) return make_uint4(0, 0, 0, 0);
-    if (width >= E) {
-        const int from = min(c, width - E);
-        uint64_t v[2];
-        __builtin_memcpy(v, row + from, 16);
-        const int drop = 8 * (int)sizeof(T) * (c - from);   // bits of the elements before c
-        if (drop != 0) {
-            const bool far = drop >= 64;
-            const int by = drop & 63;
-            const uint64_t lo = far ? v[1] : v[0], hi = far ? 0 : v[1];
-            v[0] = (lo >> by) | (by ? hi << (64 - by) : 0);
-            v[1] = hi >> by;
-        }
-        return make_uint4((uint32_t)v[0], (uint32_t)(v[0] >> 32), (uint32_t)v[1], (uint32_t)(v[1] >> 32));
-    }
-    T t[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        if (c + i < width) t[i] = row[c + i];
-        else from_f32(0.0f, t + i);
-    }
-    return __builtin_bit_cast(uint4, t);
 }
 
 // Four consecutive outputs of a row from column c on.

@@ -320,7 +320,8 @@ LINEAR4 = [   # n, m, k, d_in, d_out, group, dtype
     (1, 1, 1, 1, 1, 32, "f32"), (1, 2, 16, 256, 100, 128, "bf16"), (1, 8, 8, 4096, 64, 128, "f16"),
     (5, 3, 7, 77, 93, 32, "f16"), (24, 4, 64, 128, 256, 64, "bf16"), (32, 2, 3, 130, 31, 64, "f32"),
     (33, 16, 20, 96, 48, 32, "bf16"), (100, 2, 4, 512, 40, 32, "f16"), (3, 2, 4, 1056, 17, 128, "f32"),
-    (1024, 1, 2, 32, 8, 32, "bf16"),
+    (1024, 1, 2, 32, 8, 32, "bf16"), (16, 16, 100, 1024, 32, 32, "f16"), (9, 2, 5, 4128, 20, 64, "bf16"),
+    (2, 1, 3, 8192, 17, 64, "f16"), (1, 1, 2, 40_000, 5, 32, "bf16"), (1, 2, 3, 2050, 33, 128, "f32"),
 ]
 
 

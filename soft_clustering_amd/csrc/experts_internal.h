@@ -42,39 +42,54 @@ template <> __device__ __forceinline__ f32x4 mma16<float>(const uint4& a, const 
     return mfma16x16x4(__uint_as_float(a.w), __uint_as_float(b.w), c);
 }
 
-// 16 bytes of a row from byte c on, of `width` >= 16 bytes, at any alignment; zero
-// beyond the row.  The last, shorter piece of a row is cut out of the row's last 16 bytes.
-__device__ __forceinline__ uint4 load_bytes(const char* row, int64_t c, int64_t width) {
-    if (c >= width) return make_uint4(0, 0, 0, 0);
+static __device__ __constant__ uint4 zero_piece = {0, 0, 0, 0};
+
+// The 16 bytes from byte c of a row of `width` >= 16 on, at the alignment given, in two steps so
+// that many loads can be in flight: the load itself (of the row's last 16 bytes where fewer are left, of zeros
+// where there is none), and the bits that lie before c, to be dropped later.
+struct Loose {
+    uint4 v;
+    int drop;
+};
+template <int ALIGN>
+__device__ __forceinline__ Loose load_loose(const char* row, bool there, int64_t c, int64_t width, const char* zero) {
+    there = there && c < width;
     const int64_t from = min(c, width - 16);
-    uint64_t v[2];
-    __builtin_memcpy(v, row + from, 16);
-    const int drop = 8 * (int)(c - from);   // bits before c
-    if (drop != 0) {
-        const bool far = drop >= 64;
-        const int by = drop & 63;
-        const uint64_t lo = far ? v[1] : v[0], hi = far ? 0 : v[1];
-        v[0] = (lo >> by) | (by ? hi << (64 - by) : 0);
-        v[1] = hi >> by;
-    }
+    Loose l;
+    __builtin_memcpy(&l.v, __builtin_assume_aligned(there ? row + from : zero, ALIGN), 16);
+    l.drop = there ? 8 * (int)(c - from) : 0;
+    return l;
+}
+__device__ __forceinline__ uint4 settle(const Loose& l) {
+    uint64_t v[2] = {l.v.x | (uint64_t)l.v.y << 32, l.v.z | (uint64_t)l.v.w << 32};
+    const bool far = l.drop >= 64;
+    const int by = l.drop & 63;
+    const uint64_t lo = far ? v[1] : v[0], hi = far ? 0 : v[1];
+    v[0] = (lo >> by) | (by ? hi << (64 - by) : 0);
+    v[1] = hi >> by;
     return make_uint4((uint32_t)v[0], (uint32_t)(v[0] >> 32), (uint32_t)v[1], (uint32_t)(v[1] >> 32));
 }
 
-// 16 bytes of a row from element c on, of `width` elements, at any alignment of the elements; zero
-// beyond the row.
-template <typename T> __device__ __forceinline__ uint4 load_piece(const T* row, int c, int width) {
-    constexpr int E = Vec16<T>::kElems, S = (int)sizeof(T);
-    if (width >= E) return load_bytes((const char*)row, (int64_t)c * S, (int64_t)width * S);
+// 16 bytes of a row of less than 16, from element c on; zero beyond the row.
+template <typename T> __device__ __forceinline__ uint4 load_narrow(const T* row, bool there, int c, int width) {
+    constexpr int E = Vec16<T>::kElems;
     T t[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-        if (c + i < width) t[i] = row[c + i];
+        if (there && c + i < width) t[i] = row[c + i];
         else from_f32(0.0f, t + i);
     }
     return __builtin_bit_cast(uint4, t);
 }
 
-static __device__ __constant__ uint4 zero_piece = {0, 0, 0, 0};
+// 16 bytes of a row of any width from element c on, at any alignment of the elements; zero beyond it.
+template <typename T>
+__device__ __forceinline__ Loose load_piece(const T* row, bool there, int c, int width, const char* zero) {
+    constexpr int S = (int)sizeof(T);
+    if (width * S >= 16) return load_loose<S>((const char*)row, there, (int64_t)c * S, (int64_t)width * S, zero);
+    return Loose{load_narrow(row, there, c, width), 0};
+}
+
 
 // 16 bytes from each lane's address to LDS bytes lds + 16 lane, asynchronously: the wave that
 // issued it waits with wait_pieces() before the barrier that hands the tile over.  Written as asm

@@ -238,7 +238,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear(const 
         }
     }
     const uint32_t base = lds_address(lds);
-    uint4 ra[VEC ? 1 : AJ], rbv[VEC ? 1 : BJ];
+    Loose ra[VEC ? 1 : AJ], rb_[VEC ? 1 : BJ];
     // the pieces of the step at k0, the next one not yet fetched: VEC into buffer `buf`, else into registers
     auto fetch = [&](int k0, int buf) {
         if constexpr (VEC) {
@@ -257,16 +257,15 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear(const 
         } else {
 #pragma unroll
             for (int j = 0; j < AJ; ++j)
-                ra[j] = there_a[j] ? load_piece<T>((const T*)pa[j], k0 + ca, kd) : make_uint4(0, 0, 0, 0);
+                ra[j] = load_piece<T>((const T*)pa[j], there_a[j], k0 + ca, kd, zero);
 #pragma unroll
             for (int j = 0; j < BJ; ++j) {
-                rbv[j] = make_uint4(0, 0, 0, 0);
                 if constexpr (BACK) {
                     const int c = n0 + ((lane % CT::kPieces) ^ CT::swz(rb[j])) * E;
-                    if (there_b[j] && k0 + rb[j] < kd) rbv[j] = load_piece<T>((const T*)pb[j], c, nd);
+                    rb_[j] = load_piece<T>((const T*)pb[j], there_b[j] && k0 + rb[j] < kd, c, nd, zero);
                     pb[j] += sb[j];
-                } else if (there_b[j]) {
-                    rbv[j] = load_piece<T>((const T*)pb[j], k0 + ca, kd);
+                } else {
+                    rb_[j] = load_piece<T>((const T*)pb[j], there_b[j], k0 + ca, kd, zero);
                 }
             }
         }
@@ -274,9 +273,9 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear(const 
     auto put = [&](int buf) {
         char* to = lds + buf * kStage + lane * 16;
 #pragma unroll
-        for (int j = 0; j < AJ; ++j) *(uint4*)(to + (wave * AJ + j) * 1024) = ra[j];
+        for (int j = 0; j < AJ; ++j) *(uint4*)(to + (wave * AJ + j) * 1024) = settle(ra[j]);
 #pragma unroll
-        for (int j = 0; j < BJ; ++j) *(uint4*)(to + S::kABytes + (wave * BJ + j) * 1024) = rbv[j];
+        for (int j = 0; j < BJ; ++j) *(uint4*)(to + S::kABytes + (wave * BJ + j) * 1024) = settle(rb_[j]);
     };
 
     // blocks of columns with outputs (VEC: not worth the branches, its loads bound narrow models)
@@ -417,20 +416,21 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_linear_few(const LinArgs a) 
     const bool has_w = o < a.d_out, has_x = row >= 0;
     f32x4 acc = {};
     const int mine = (lane >> 4) * E;
+    const char* zero = zero_address();
     auto piece = [&](const T* p, bool there, int k) {
-        if (!there || k >= a.d_in) return make_uint4(0, 0, 0, 0);
-        if constexpr (VEC) return *(const uint4*)(p + k);
-        else return load_piece<T>(p, k, a.d_in);
+        if constexpr (VEC) return Loose{*(const uint4*)(there && k < a.d_in ? (const char*)(p + k) : zero), 0};
+        else return load_piece<T>(p, there, k, a.d_in, zero);
     };
     for (int k0 = wave * KS; k0 < a.d_in; k0 += kAhead * kFewWaves * KS) {
-        uint4 fw[kAhead], fx[kAhead];
+        Loose fw[kAhead], fx[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             fw[u] = piece(w, has_w, k0 + u * kFewWaves * KS + mine);
             fx[u] = piece(x, has_x, k0 + u * kFewWaves * KS + mine);
         }
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) acc = mma16<T>(fw[u], fx[u], acc);
+        for (int u = 0; u < kAhead; ++u)
+            acc = VEC ? mma16<T>(fw[u].v, fx[u].v, acc) : mma16<T>(settle(fw[u]), settle(fx[u]), acc);
     }
     part[wave][lane] = acc;
     __syncthreads();
@@ -500,7 +500,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear_dw(con
     const bool with_db = a.db != nullptr && i0 == 0 && wi == 0;
 
     const uint32_t base = lds_address(lds);
-    uint4 rx[VEC ? 1 : XJ], ry[VEC ? 1 : YJ];
+    Loose rx[VEC ? 1 : XJ], ry[VEC ? 1 : YJ];
     // Rows of x behind the slots, one slot a thread and segment of kThreads slots, two segments in
     // LDS: an entry loaded in every step would be waited for behind the pieces on their way.
     constexpr int R = S::kThreads, SPR = R / KS;   // slots, steps of a segment
@@ -541,22 +541,22 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear_dw(con
             const bool there = from >= 0 && cx[j] < a.d_in;
             const char* row = (const char*)((const T*)a.x + (int64_t)from * a.ldx);
             if constexpr (VEC) fetch_piece(there ? row + cx[j] * (int)sizeof(T) : zero, to + (wave * XJ + j) * 1024);
-            else rx[j] = there ? load_piece<T>((const T*)row, cx[j], a.d_in) : make_uint4(0, 0, 0, 0);
+            else rx[j] = load_piece<T>((const T*)row, there, cx[j], a.d_in, zero);
         }
 #pragma unroll
         for (int j = 0; j < YJ; ++j) {
             const bool there = whole || s0 - lr.s0 + rowy[j] < s1;
             if constexpr (VEC) fetch_piece(there ? py[j] : zero, to + S::kABytes + (wave * YJ + j) * 1024);
-            else ry[j] = there ? load_piece<T>((const T*)py[j], cy[j], a.d_out) : make_uint4(0, 0, 0, 0);
+            else ry[j] = load_piece<T>((const T*)py[j], there, cy[j], a.d_out, zero);
             py[j] += sy[j];
         }
     };
     auto put = [&](int buf) {
         char* to = lds + buf * kStage + lane * 16;
 #pragma unroll
-        for (int j = 0; j < XJ; ++j) *(uint4*)(to + (wave * XJ + j) * 1024) = rx[j];
+        for (int j = 0; j < XJ; ++j) *(uint4*)(to + (wave * XJ + j) * 1024) = settle(rx[j]);
 #pragma unroll
-        for (int j = 0; j < YJ; ++j) *(uint4*)(to + S::kABytes + (wave * YJ + j) * 1024) = ry[j];
+        for (int j = 0; j < YJ; ++j) *(uint4*)(to + S::kABytes + (wave * YJ + j) * 1024) = settle(ry[j]);
     };
 
     const bool live[2] = {VEC || i0 + wi < a.d_in, VEC || i0 + wi + 32 < a.d_in};   // blocks with gradients

@@ -149,7 +149,7 @@ template <bool VEC, int BYTES> struct Rows {
         } else {
             uint4 v = make_uint4(0, 0, 0, 0);
             if (from != nullptr && width >= 16) {
-                v = load_bytes(from, b, width);
+                v = settle(load_loose<1>(from, true, b, width, (const char*)&zero_piece));
             } else if (from != nullptr) {
                 uint8_t t[16];
 #pragma unroll

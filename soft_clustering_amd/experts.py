@@ -76,16 +76,19 @@ def _declare():
 _declare()
 
 
-def _call(fn, device, stream, tensors, launch):
-    """launch(raw stream) with `device` current, on `stream` (default: the
+_I32, _F32 = torch.int32, torch.float32
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
+def _call(fn, index, stream, tensors, launch):
+    """launch(raw stream) with device `index` current, on `stream` (default: the
     device's current one).  On another stream than the current one, memory
     allocated by launch belongs to it, and the caller's tensors are marked as
     in use there."""
-    index = device.index
-    if torch._C._cuda_getDevice() != index:
+    if _current_device() != index:
         with torch.cuda.device(index):
-            return _call(fn, device, stream, tensors, launch)
-    raw = torch._C._cuda_getCurrentRawStream(index)
+            return _call(fn, index, stream, tensors, launch)
+    raw = _raw_stream(index)
     if stream is None or stream.cuda_stream == raw:
         return launch(raw)
     if stream.device.index != index:
@@ -101,31 +104,41 @@ def _fail(fn, what):
     raise ValueError(f"{fn}: {what}")
 
 
-def _same_device(fn, first, *others):
-    if not first.is_cuda:
-        _fail(fn, "tensors must be on a GPU")
-    for t in others:
-        if t is not None and t.device != first.device:
-            _fail(fn, "tensors must be on one device")
+def _device_of(fn, tensors):
+    """Index of the one GPU that holds the tensors (None: not given)."""
+    index = None
+    for t in tensors:
+        if t is not None:
+            i = t.get_device()
+            if index is None:
+                if i < 0 or not t.is_cuda:
+                    _fail(fn, "tensors must be on a GPU")
+                index = i
+            elif i != index:
+                _fail(fn, "tensors must be on one device")
+    return index
 
 
 def _flat(fn, name, t, dtype, shape):
     """A contiguous tensor of this type and shape."""
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         _fail(fn, f"{name} must be a contiguous {dtype} tensor of shape {shape}")
 
 
 def _rows(fn, name, t, rows, width, dtype):
     """Row stride of a 2-D tensor of `rows` rows with unit column stride."""
-    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width:
+    if t.dtype is not dtype or t.shape != (rows, width):
         _fail(fn, f"{name} must be a {dtype} tensor of shape ({rows}, {width})")
-    if width > 1 and t.stride(1) != 1:
+    if rows <= 1 and width <= 1:
+        return width
+    ld, step = t.stride()
+    if width > 1 and step != 1:
         _fail(fn, f"{name} must have unit column stride")
     if rows <= 1:
         return width
-    if t.stride(0) < width:
+    if ld < width:
         _fail(fn, f"the rows of {name} must not overlap")
-    return t.stride(0)
+    return ld
 
 
 def _code(fn, t):
@@ -138,14 +151,14 @@ def _code(fn, t):
 def _lists(fn, routes):
     """(n, m, k, C struct) of checked lists."""
     offsets, entry, slot = routes
-    if slot.dim() != 2 or entry.dim() != 1 or offsets.dim() != 1 or entry.shape[0] != slot.shape[0] * slot.shape[1]:
+    shape, lists = slot.shape, offsets.shape
+    if len(shape) != 2 or len(lists) != 1 or entry.shape != (shape[0] * shape[1],):
         _fail(fn, "routes must be offsets [k + 1], entry [n * m], slot [n, m]")
-    if offsets.dtype != torch.int32 or entry.dtype != torch.int32 or slot.dtype != torch.int32 or not (
-            offsets.is_contiguous() and entry.is_contiguous() and slot.is_contiguous()):
+    if not (offsets.dtype is entry.dtype is slot.dtype is _I32 and offsets.is_contiguous() and entry.is_contiguous()
+            and slot.is_contiguous()):
         _fail(fn, "routes must be contiguous int32 tensors")
-    _same_device(fn, slot, offsets, entry)
-    n, m = slot.shape
-    k = offsets.shape[0] - 1
+    n, m = shape
+    k = lists[0] - 1
     return n, m, k, _CRoutes(n, m, k, offsets.data_ptr(), entry.data_ptr(), slot.data_ptr())
 
 
@@ -172,10 +185,10 @@ def route(idx, k, out=None, stream=None) -> Routes:
     need = ctypes.c_size_t(0)
     _check(_lib.gmm_route_workspace_bytes(n, m, k, ctypes.byref(need)), "gmm_route_workspace_bytes")
     if out is not None:
-        _flat("route", "offsets", out.offsets, torch.int32, (k + 1,))
-        _flat("route", "entry", out.entry, torch.int32, (n * m,))
-        _flat("route", "slot", out.slot, torch.int32, (n, m))
-    _same_device("route", idx, *(out or ()))
+        _flat("route", "offsets", out.offsets, _I32, (k + 1,))
+        _flat("route", "entry", out.entry, _I32, (n * m,))
+        _flat("route", "slot", out.slot, _I32, (n, m))
+    index = _device_of("route", (idx, *(out or ())))
 
     def launch(raw):
         r = out
@@ -186,7 +199,7 @@ def route(idx, k, out=None, stream=None) -> Routes:
         _check(_lib.gmm_route(n, m, k, idx.data_ptr(), ws, need.value, r.offsets.data_ptr(), r.entry.data_ptr(),
                               r.slot.data_ptr(), raw), "gmm_route")
         return r
-    return _call("route", idx.device, stream, (idx, *(out or ())), launch)
+    return _call("route", index, stream, (idx, *(out or ())), launch)
 
 
 def _one_output(fn, lib_fn, routes, src, src_rows, out, out_rows, gamma, stream):
@@ -198,15 +211,16 @@ def _one_output(fn, lib_fn, routes, src, src_rows, out, out_rows, gamma, stream)
     ld_in = _rows(fn, "the input", src, src_rows(n, m), d, src.dtype)
     ld_out = d if out is None else _rows(fn, "out", out, out_rows(n, m), d, src.dtype)
     if gamma is not None:
-        _flat(fn, "gamma", gamma, torch.float32, (n, m))
-    _same_device(fn, routes.slot, src, out, gamma)
+        _flat(fn, "gamma", gamma, _F32, (n, m))
+    tensors = (*routes, src, out, gamma)
+    index = _device_of(fn, tensors)
 
     def launch(raw):
         o = torch.empty((out_rows(n, m), d), dtype=src.dtype, device=src.device) if out is None else out
         weights = () if gamma is None else (gamma.data_ptr(),)
         _check(lib_fn(ctypes.byref(c), d, code, src.data_ptr(), ld_in, *weights, o.data_ptr(), ld_out, raw), fn)
         return o
-    return _call(fn, src.device, stream, (*routes, src, out, gamma), launch)
+    return _call(fn, index, stream, tensors, launch)
 
 
 def _by_point(n, m):
@@ -248,11 +262,12 @@ def combine_backward(dout, z, gamma, routes, dz=None, dgamma=None, need=(True, T
     if need_g and z is None:
         _fail(fn, "z is needed for dgamma")
     ldz = _rows(fn, "z", z, n * m, d, dout.dtype) if need_g else d
-    _flat(fn, "gamma", gamma, torch.float32, (n, m))
+    _flat(fn, "gamma", gamma, _F32, (n, m))
     lddz = d if dz is None else _rows(fn, "dz", dz, n * m, d, dout.dtype)
     if dgamma is not None:
-        _flat(fn, "dgamma", dgamma, torch.float32, (n, m))
-    _same_device(fn, routes.slot, dout, z, gamma, dz, dgamma)
+        _flat(fn, "dgamma", dgamma, _F32, (n, m))
+    tensors = (*routes, dout, z, gamma, dz, dgamma)
+    index = _device_of(fn, tensors)
 
     def launch(raw):
         oz, og = dz if need_z else None, dgamma if need_g else None
@@ -263,7 +278,7 @@ def combine_backward(dout, z, gamma, routes, dz=None, dgamma=None, need=(True, T
         _check(_lib.gmm_combine_backward(ctypes.byref(c), d, code, dout.data_ptr(), lddo, _ptr(z) if need_g else None,
                                          ldz, gamma.data_ptr(), _ptr(oz), lddz, _ptr(og), raw), fn)
         return oz, og
-    return _call(fn, dout.device, stream, (*routes, dout, z, gamma, dz, dgamma), launch)
+    return _call(fn, index, stream, tensors, launch)
 
 
 def linear(x, w, bias, routes, sorted_rows=False, out=None, stream=None):
@@ -279,9 +294,10 @@ def linear(x, w, bias, routes, sorted_rows=False, out=None, stream=None):
     _flat(fn, "w", w, x.dtype, (k, do, di))
     ldx = _rows(fn, "x", x, n * m if sorted_rows else n, di, x.dtype)
     if bias is not None:
-        _flat(fn, "bias", bias, torch.float32, (k, do))
+        _flat(fn, "bias", bias, _F32, (k, do))
     ldy = do if out is None else _rows(fn, "out", out, n * m, do, x.dtype)
-    _same_device(fn, routes.slot, x, w, bias, out)
+    tensors = (*routes, x, w, bias, out)
+    index = _device_of(fn, tensors)
     desc = _CLinear(di, do, ldx, ldy, di, code, 1 if sorted_rows else 0)
 
     def launch(raw):
@@ -289,7 +305,7 @@ def linear(x, w, bias, routes, sorted_rows=False, out=None, stream=None):
         _check(_lib.gmm_linear(ctypes.byref(c), ctypes.byref(desc), x.data_ptr(), w.data_ptr(), _ptr(bias),
                                y.data_ptr(), raw), fn)
         return y
-    return _call(fn, x.device, stream, (*routes, x, w, bias, out), launch)
+    return _call(fn, index, stream, tensors, launch)
 
 
 def linear_backward(dy, x, w, routes, sorted_rows=False, dx=None, dw=None, db=None, need=(True, True, True),
@@ -318,8 +334,9 @@ def linear_backward(dy, x, w, routes, sorted_rows=False, dx=None, dw=None, db=No
     if dw is not None:
         _flat(fn, "dw", dw, torch.float32, shape)
     if db is not None:
-        _flat(fn, "db", db, torch.float32, (k, do))
-    _same_device(fn, routes.slot, dy, x, wt, dx, dw, db)
+        _flat(fn, "db", db, _F32, (k, do))
+    tensors = (*routes, dy, x, wt, dx, dw, db)
+    index = _device_of(fn, tensors)
     desc = _CLinear(di, do, ldx, lddy, lddx, code, 1 if sorted_rows else 0)
     ws_bytes = ctypes.c_size_t(0)
     if need_w:
@@ -339,7 +356,7 @@ def linear_backward(dy, x, w, routes, sorted_rows=False, dx=None, dw=None, db=No
                                         _ptr(x) if need_w else None, _ptr(wt) if need_x else None, _ptr(ox), _ptr(ow),
                                         _ptr(ob), ws, ws_bytes.value, raw), fn)
         return ox, ow, ob
-    return _call(fn, dy.device, stream, (*routes, dy, x, wt, dx, dw, db), launch)
+    return _call(fn, index, stream, tensors, launch)
 
 
 def quantize4(w, group=128, stream=None):
@@ -349,7 +366,7 @@ def quantize4(w, group=128, stream=None):
     code = _code(fn, w)
     if w.dim() < 1 or not w.is_contiguous():
         _fail(fn, "w must be contiguous, [..., d_in]")
-    _same_device(fn, w)
+    index = _device_of(fn, (w,))
     d_in = w.shape[-1]
     rows = w.numel() // d_in if d_in else 0
 
@@ -360,7 +377,7 @@ def quantize4(w, group=128, stream=None):
         _check(_lib.gmm_quantize4(rows, d_in, int(group), code, w.data_ptr(), codes.data_ptr(), scales.data_ptr(),
                                   raw), "gmm_quantize4")
         return codes, scales
-    return _call(fn, w.device, stream, (w,), launch)
+    return _call(fn, index, stream, (w,), launch)
 
 
 def linear4(x, idx, gamma, codes, scales, group=128, bias=None, out=None, stream=None):
@@ -378,18 +395,19 @@ def linear4(x, idx, gamma, codes, scales, group=128, bias=None, out=None, stream
     if group not in (32, 64, 128):
         _fail(fn, "group must be 32, 64 or 128")
     ldx = _rows(fn, "x", x, n, di, x.dtype)
-    _flat(fn, "idx", idx, torch.int32, (n, m))
-    _flat(fn, "gamma", gamma, torch.float32, (n, m))
+    _flat(fn, "idx", idx, _I32, (n, m))
+    _flat(fn, "gamma", gamma, _F32, (n, m))
     _flat(fn, "codes", codes, torch.uint8, (k, do, (di + 1) // 2))
     _flat(fn, "scales", scales, torch.bfloat16, (k, do, -(-di // group)))
     if bias is not None:
-        _flat(fn, "bias", bias, torch.float32, (k, do))
+        _flat(fn, "bias", bias, _F32, (k, do))
     ldo = do if out is None else _rows(fn, "out", out, n, do, x.dtype)
-    _same_device(fn, x, idx, gamma, codes, scales, bias, out)
+    tensors = (x, idx, gamma, codes, scales, bias, out)
+    index = _device_of(fn, tensors)
 
     def launch(raw):
         o = torch.empty((n, do), dtype=x.dtype, device=x.device) if out is None else out
         _check(_lib.gmm_linear4(n, m, k, di, do, group, code, x.data_ptr(), ldx, idx.data_ptr(), gamma.data_ptr(),
                                 codes.data_ptr(), scales.data_ptr(), _ptr(bias), o.data_ptr(), ldo, raw), fn)
         return o
-    return _call(fn, x.device, stream, (x, idx, gamma, codes, scales, bias, out), launch)
+    return _call(fn, index, stream, tensors, launch)

@@ -160,7 +160,7 @@ struct LinArgs {
     const float* bias;
     void* c;             // y or dx
     int64_t ldc;
-    int row_blocks, col_blocks;
+    int row_blocks, col_blocks, col_step;
 };
 
 // Row of x behind an entry, or -1.
@@ -191,7 +191,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear(const 
     const ListRows lr = find_rows(a.offsets, a.K, a.rows, tile / a.col_blocks, S::kM, a.by_slot);
     if (lr.k < 0) return;
     const int kd = BACK ? a.d_out : a.d_in, nd = BACK ? a.d_in : a.d_out;   // contraction, output width
-    const int n0 = tile % a.col_blocks * S::kN;
+    const int n0 = tile % a.col_blocks * a.col_step, n1 = min(n0 + a.col_step, nd);   // this tile's outputs
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = wave % WM * 64, wn = wave / WM * 64;
     const T* w = (const T*)a.w + (int64_t)lr.k * a.d_in * a.d_out;
@@ -225,14 +225,14 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear(const 
     for (int j = 0; j < BJ; ++j) {
         if constexpr (!BACK) {
             const int r = n0 + RA * (wave * BJ + j) + lane / PA;
-            there_b[j] = r < nd;
+            there_b[j] = r < n1;
             pb[j] = there_b[j] ? (const char*)(w + (int64_t)r * kd + (VEC ? ca : 0)) : zero;
             sb[j] = there_b[j] ? kStep : 0;
             rb[j] = 0;
         } else {
             rb[j] = (wave * BJ + j) * RI + lane / CT::kPieces;
             const int c = n0 + ((lane % CT::kPieces) ^ CT::swz(rb[j])) * E;
-            there_b[j] = c < nd;
+            there_b[j] = c < n1;
             pb[j] = there_b[j] ? (const char*)(w + (int64_t)rb[j] * nd + (VEC ? c : 0)) : zero;
             sb[j] = there_b[j] ? (int64_t)KS * nd * (int)sizeof(T) : 0;
         }
@@ -278,25 +278,27 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear(const 
         for (int j = 0; j < BJ; ++j) *(uint4*)(to + S::kABytes + (wave * BJ + j) * 1024) = settle(rb_[j]);
     };
 
-    // blocks of columns with outputs (VEC: not worth the branches, its loads bound narrow models)
-    const bool live[2] = {VEC || n0 + wn < nd, VEC || n0 + wn + 32 < nd};
+    // blocks of columns with outputs (16-bit pieces: not worth the branches)
+    constexpr bool kAll = VEC && sizeof(T) == 2;
+    const bool live[2] = {kAll || n0 + wn < n1, kAll || n0 + wn + 32 < n1};
     f32x16 acc[2][2] = {};
     if (!BACK && a.bias != nullptr) {   // sums start from the bias
         const float* bias = a.bias + (int64_t)lr.k * nd;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
+            if constexpr (VEC) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int c = n0 + wn + 32 * h + 8 * q + 4 * (lane >> 5);
-                float b[4];
-                if constexpr (VEC) {
+                for (int q = 0; q < 4; ++q) {
+                    const int c = n0 + wn + 32 * h + 8 * q + 4 * (lane >> 5);
+                    float b[4];
                     __builtin_memcpy(b, bias + (c < nd ? c : 0), sizeof(b));
-                } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) b[e] = bias[min(c + e, nd - 1)];
+                    for (int e = 0; e < 4; ++e) acc[0][h][4 * q + e] = acc[1][h][4 * q + e] = b[e];
                 }
+            } else {
+                const float b = bias[min(n0 + wn + 32 * h + (lane & 31), nd - 1)];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[0][h][4 * q + e] = acc[1][h][4 * q + e] = b[e];
+                for (int r = 0; r < 16; ++r) acc[0][h][r] = acc[1][h][r] = b;
             }
     }
     const int steps = (kd + KS - 1) / KS;
@@ -327,14 +329,15 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear(const 
             for (int h = 0; h < 2; ++h)
                 if (live[h]) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) acc[i][h] = mma<T>(fb[h], fa[i], acc[i][h]);
+                    for (int i = 0; i < 2; ++i)   // VEC: lanes along the slots, else along the columns
+                        acc[i][h] = VEC ? mma<T>(fb[h], fa[i], acc[i][h]) : mma<T>(fa[i], fb[h], acc[i][h]);
                 }
         }
         buf = buf + 1 < kStages ? buf + 1 : 0;
     }
 
-    // lane: slot lane % 32, four consecutive outputs per register group
     if constexpr (VEC) {
+        // lane: slot lane % 32, four consecutive outputs per register group;
         // through LDS, so that a row leaves in whole pieces: the wave's 64 x 64 block, two halves of
         // 32 rows, pieces swizzled by the row
         constexpr int RB = 64 * (int)sizeof(T), PR = RB / 16;   // bytes, pieces of a row
@@ -366,26 +369,25 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear(const 
             T* to = (T*)a.c + (int64_t)s * a.ldc + c;
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (s + RU * u < lr.s1 && c < nd) *(uint4*)(to + (int64_t)(RU * u) * a.ldc) = v[u];
+                if (s + RU * u < lr.s1 && c < n1) *(uint4*)(to + (int64_t)(RU * u) * a.ldc) = v[u];
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
         }
     } else {
+        // lane: output lane % 32, slots 8 (r / 4) + 4 (lane / 32) + r % 4: a register's store covers 32
+        // outputs of two rows
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int s = lr.s0 + wm + 32 * i + (lane & 31);
-            if (s >= lr.s1) continue;
-            T* row = (T*)a.c + (int64_t)s * a.ldc;
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int r = 0; r < 16; ++r) {
+                const int s = lr.s0 + wm + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+                if (s >= lr.s1) continue;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float v[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = acc[i][h][4 * q + e];
-                    store4<T, false>(row, n0 + wn + 32 * h + 8 * q + 4 * (lane >> 5), nd, v);
+                for (int h = 0; h < 2; ++h) {
+                    const int c = n0 + wn + 32 * h + (lane & 31);
+                    if (c < n1) from_f32(acc[i][h][r], (T*)a.c + (int64_t)s * a.ldc + c);
                 }
-        }
+            }
     }
 }
 
@@ -464,7 +466,7 @@ struct GradArgs {
     float* dw;
     float* db;
     float* part;            // slots of d_out * d_in + d_out sums
-    int row_blocks, in_blocks, out_blocks;
+    int row_blocks, in_blocks, out_blocks, in_step, out_step;
 };
 
 // First partial slot of a list of more than one chunk that starts at slot a:
@@ -485,14 +487,15 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear_dw(con
     __shared__ int source[2 * S::kThreads];
     const int per_row = a.in_blocks * a.out_blocks;
     // The lists' lengths differ, so each XCD takes an eighth of the tiles of every chunk (a run of
-    // them, which shares rows of x and dy); with fewer than 8 tiles, every eighth tile.
+    // them, which shares rows of x and dy); with fewer than 8 tiles, each tile goes round the XCDs.
     const int per = (per_row + 7) >> 3, b = blockIdx.x;
     const int block = per_row < 8 ? b / per_row : (b >> 3) / per;
-    const int tile = per_row < 8 ? b % per_row : (b & 7) * per + (b >> 3) % per;
+    const int tile = per_row < 8 ? (b % per_row + (int)((int64_t)block * per_row >> 3)) % per_row : (b & 7) * per + (b >> 3) % per;
     if (block >= a.row_blocks || tile >= per_row) return;
     const ListRows lr = find_rows(a.offsets, a.K, a.rows, block, a.chunk, a.by_slot);
     if (lr.k < 0) return;
-    const int i0 = tile % a.in_blocks * S::kM, o0 = tile / a.in_blocks * S::kN;
+    const int i0 = tile % a.in_blocks * a.in_step, o0 = tile / a.in_blocks * a.out_step;
+    const int i1 = min(i0 + a.in_step, a.d_in), o1 = min(o0 + a.out_step, a.d_out);   // this tile's weights
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wi = wave % WM * 64, wo = wave / WM * 64;
     const int first = lr.first;
@@ -527,7 +530,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear_dw(con
     for (int j = 0; j < YJ; ++j) {
         rowy[j] = lr.s0 + (wave * YJ + j) * YR + lane / YT::kPieces;
         cy[j] = o0 + ((lane % YT::kPieces) ^ YT::swz((wave * YJ + j) * YR + lane / YT::kPieces)) * E;
-        const bool there = cy[j] < a.d_out;
+        const bool there = cy[j] < o1;
         py[j] = there ? (const char*)((const T*)a.dy + (int64_t)rowy[j] * a.ldy + (VEC ? cy[j] : 0)) : zero;
         sy[j] = there ? (int64_t)KS * a.ldy * (int)sizeof(T) : 0;
     }
@@ -538,7 +541,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear_dw(con
 #pragma unroll
         for (int j = 0; j < XJ; ++j) {
             const int from = source[(s0 - lr.s0 + (wave * XJ + j) * XR + lane / XT::kPieces) & (2 * R - 1)];
-            const bool there = from >= 0 && cx[j] < a.d_in;
+            const bool there = from >= 0 && cx[j] < i1;
             const char* row = (const char*)((const T*)a.x + (int64_t)from * a.ldx);
             if constexpr (VEC) fetch_piece(there ? row + cx[j] * (int)sizeof(T) : zero, to + (wave * XJ + j) * 1024);
             else rx[j] = load_piece<T>((const T*)row, there, cx[j], a.d_in, zero);
@@ -559,7 +562,10 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear_dw(con
         for (int j = 0; j < YJ; ++j) *(uint4*)(to + S::kABytes + (wave * YJ + j) * 1024) = settle(ry[j]);
     };
 
-    const bool live[2] = {VEC || i0 + wi < a.d_in, VEC || i0 + wi + 32 < a.d_in};   // blocks with gradients
+    // blocks with gradients (16-bit pieces: not worth the branches)
+    constexpr bool kAll = VEC && sizeof(T) == 2;
+    const bool live[2] = {kAll || i0 + wi < i1, kAll || i0 + wi + 32 < i1};
+    const bool live_o[2] = {kAll || o0 + wo < o1, kAll || o0 + wo + 32 < o1};
     f32x16 acc[2][2] = {};
     f32x4 sum[2] = {};
     const uint4 ones = row_sums<T>();
@@ -595,10 +601,9 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear_dw(con
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                if (live[i]) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) acc[i][h] = mma<T>(fy[h], fx[i], acc[i][h]);
-                }
+                for (int h = 0; h < 2; ++h)
+                    if (live[i] && live_o[h]) acc[i][h] = mma<T>(fy[h], fx[i], acc[i][h]);
             if (with_db) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) sum[h] = mma16<T>(ones, fy[h], sum[h]);
@@ -620,7 +625,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear_dw(con
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-                if (o0 + wo + 32 * h + 16 * r + lane < a.d_out) db[o0 + wo + 32 * h + 16 * r + lane] = sum[h][r];
+                if (o0 + wo + 32 * h + 16 * r + lane < o1) db[o0 + wo + 32 * h + 16 * r + lane] = sum[h][r];
     }
     // lane: input i = lane % 32, so that a register's store covers 128 bytes of two rows; outputs
     // 8 (r / 4) + 4 (lane / 32) + r % 4
@@ -629,11 +634,11 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear_dw(con
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             const int o = o0 + wo + 32 * h + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-            if (o >= a.d_out) continue;
+            if (o >= o1) continue;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int c = i0 + wi + 32 * i + (lane & 31);
-                if (c < a.d_in) dw[(int64_t)o * a.d_in + c] = acc[i][h][r];
+                if (c < i1) dw[(int64_t)o * a.d_in + c] = acc[i][h][r];
             }
         }
 }
@@ -685,6 +690,12 @@ int chunk_rows(int64_t rows, const gmm_linear_desc* d) {
 
 int blocks_of(int width, int tile) { return (width + tile - 1) / tile; }
 
+// Columns of each of a width's tiles: as even as blocks of 32 allow (130: 96 and 34, not 128 and 2).
+int step_of(int width, int tile) {
+    const int blocks = blocks_of(width, tile);
+    return ((width + blocks - 1) / blocks + 31) / 32 * 32;
+}
+
 gmm_status check_desc(const gmm_linear_desc* d) {
     if (d == nullptr) return GMM_E_ARG;
     gmm_status st = check_width(d->d_in, d->dtype);
@@ -705,7 +716,9 @@ gmm_status launch_shape(const LinArgs& a, hipStream_t stream) {
     LinArgs b = a;
     int grid;
     b.row_blocks = (int)row_blocks(a.rows, a.K, S::kM, &b.by_slot);
-    b.col_blocks = blocks_of(BACK ? a.d_in : a.d_out, S::kN);
+    const int nd = BACK ? a.d_in : a.d_out;
+    b.col_blocks = blocks_of(nd, S::kN);
+    b.col_step = step_of(nd, S::kN);
     const gmm_status st = grid_of((int64_t)b.row_blocks * b.col_blocks, &grid);
     if (st != GMM_OK) return st;
     hipLaunchKernelGGL((k_linear<T, VEC, BACK, S>), dim3(grid), dim3(S::kThreads), 0, stream, b);
@@ -769,6 +782,7 @@ template <typename T, bool VEC, typename S> gmm_status launch_dw_shape(const Gra
     int grid;
     b.row_blocks = (int)row_blocks(a.rows, a.K, a.chunk, &b.by_slot);
     b.in_blocks = blocks_of(a.d_in, S::kM), b.out_blocks = blocks_of(a.d_out, S::kN);
+    b.in_step = step_of(a.d_in, S::kM), b.out_step = step_of(a.d_out, S::kN);
     const int64_t per = (int64_t)b.in_blocks * b.out_blocks;
     const gmm_status st = grid_of(b.row_blocks * (per < 8 ? per : (per + 7) / 8 * 8), &grid);
     if (st != GMM_OK) return st;
@@ -814,7 +828,7 @@ gmm_status gmm_linear(const gmm_routes* routes, const gmm_linear_desc* desc, con
     if (routes->n == 0) return GMM_OK;
     if (x == nullptr || w == nullptr || y == nullptr) return GMM_E_ARG;
     LinArgs a = {routes->offsets, routes->entry, (int)(routes->n * routes->m), routes->k, magic_of(routes->m), false,
-                 desc->sorted_rows == 0, x, desc->ldx, w, (int)desc->d_in, (int)desc->d_out, bias, y, desc->ldy, 0, 0};
+                 desc->sorted_rows == 0, x, desc->ldx, w, (int)desc->d_in, (int)desc->d_out, bias, y, desc->ldy, 0, 0, 0};
     const int es = elem_size(desc->dtype);
     const bool vec = desc->d_in * es % 16 == 0 && desc->ldx * es % 16 == 0 && aligned16(x) && aligned16(w) &&
                      desc->d_out * es % 16 == 0 && desc->ldy * es % 16 == 0 && aligned16(y);
@@ -858,7 +872,7 @@ gmm_status gmm_linear_backward(const gmm_routes* routes, const gmm_linear_desc* 
     const bool dy_vec = desc->ldy * es % 16 == 0 && aligned16(dy);
     if (dx != nullptr && rows > 0) {
         LinArgs a = {routes->offsets, routes->entry, (int)rows, routes->k, magic_of(routes->m), false, false, dy,
-                     desc->ldy, w, (int)desc->d_in, (int)desc->d_out, nullptr, dx, desc->lddx, 0, 0};
+                     desc->ldy, w, (int)desc->d_in, (int)desc->d_out, nullptr, dx, desc->lddx, 0, 0, 0};
         const bool vec = wide && dy_vec && aligned16(w) && desc->lddx * es % 16 == 0 && aligned16(dx);
         if ((st = run_linear<true>(a, desc->dtype, vec, stream)) != GMM_OK) return st;
     }
@@ -871,7 +885,7 @@ gmm_status gmm_linear_backward(const gmm_routes* routes, const gmm_linear_desc* 
     }
     GradArgs g = {routes->offsets, routes->entry, (int)rows, routes->k, magic_of(routes->m), false,
                   desc->sorted_rows == 0, chunk_rows(rows, desc), x, desc->ldx, dy, desc->ldy, (int)desc->d_in,
-                  (int)desc->d_out, dw, db, (float*)ws, 0, 0, 0};
+                  (int)desc->d_out, dw, db, (float*)ws, 0, 0, 0, 0, 0};
     const bool vec = wide && dy_vec && desc->ldx * es % 16 == 0 && aligned16(x) && aligned16(dw);
     switch (desc->dtype) {
         case GMM_F32: return vec ? launch_dw<float, true>(g, stream) : launch_dw<float, false>(g, stream);

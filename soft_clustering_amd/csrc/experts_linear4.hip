@@ -15,7 +15,7 @@
 // the component, and added in fp32.  The halves of a word of codes are
 // nibbles i and i + 4, so x takes the same order.  fp16: 0x6400 | q is 1024 + q, less 1032.  bf16:
 // 0x4300 | q is 128 + q, and a second product with -136 takes the offset off.  fp32 rows are
-// split into three bf16 parts, which hold all 24 bits.
+// split into three bf16 parts, which hold all 24 bits, and meet q - 8 in bf16.
 
 #include <type_traits>
 
@@ -68,6 +68,23 @@ __device__ __forceinline__ Bits bits_of(uint32_t one) {
 }
 __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) { return (v & mask) | bits; }
 
+// q - 8 of a word of codes in fp16: 1024 + q - 1032, and (1024 + 16 q) / 16 - 72, all exact.
+__device__ __forceinline__ uint4 codes_f16(uint32_t q, const Bits& b) {
+    typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+    const half2v less = {(_Float16)-1032.0f, (_Float16)-1032.0f}, less16 = {(_Float16)-72.0f, (_Float16)-72.0f},
+                 by16 = {(_Float16)0.0625f, (_Float16)0.0625f};
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const half2v lo = __builtin_bit_cast(half2v, and_or(q, b.low, b.one)),
+                     hi = __builtin_bit_cast(half2v, and_or(q, b.high, b.one));
+        w[2 * i] = __builtin_bit_cast(uint32_t, lo + less);
+        w[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(hi, by16, less16));
+        q >>= 8;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Products of one word of codes with the eight values of x it meets.
 template <typename T> struct Codes;
 template <> struct Codes<_Float16> {
@@ -75,20 +92,7 @@ template <> struct Codes<_Float16> {
     static constexpr uint32_t kOne = 0x64006400u;   // 1024
     __device__ __forceinline__ static void take(const uint4* v, uint4* f) { f[0] = code_order(v[0]); }
     __device__ __forceinline__ static f32x4 mul(const uint4* f, uint32_t q, const Bits& b, f32x4 d) {
-        // 1024 + q - 1032, and (1024 + 16 q) / 16 - 72: all exact
-        typedef _Float16 half2v __attribute__((ext_vector_type(2)));
-        const half2v less = {(_Float16)-1032.0f, (_Float16)-1032.0f}, less16 = {(_Float16)-72.0f, (_Float16)-72.0f},
-                     by16 = {(_Float16)0.0625f, (_Float16)0.0625f};
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const half2v lo = __builtin_bit_cast(half2v, and_or(q, b.low, b.one)),
-                         hi = __builtin_bit_cast(half2v, and_or(q, b.high, b.one));
-            w[2 * i] = __builtin_bit_cast(uint32_t, lo + less);
-            w[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(hi, by16, less16));
-            q >>= 8;
-        }
-        return mma16<_Float16>(f[0], make_uint4(w[0], w[1], w[2], w[3]), d);
+        return mma16<_Float16>(f[0], codes_f16(q, b), d);
     }
 };
 __device__ __forceinline__ uint4 codes_bf16(uint32_t q, const Bits& b) {
@@ -109,7 +113,7 @@ template <> struct Codes<bf16_t> {
 };
 template <> struct Codes<float> {
     static constexpr int kTerms = 3;
-    static constexpr uint32_t kOne = 0x43004300u;
+    static constexpr uint32_t kOne = 0x64006400u;
     __device__ __forceinline__ static void take(const uint4* raw, uint4* f) {
         float v[8];
 #pragma unroll
@@ -127,8 +131,12 @@ template <> struct Codes<float> {
         }
     }
     __device__ __forceinline__ static f32x4 mul(const uint4* f, uint32_t q, const Bits& b, f32x4 d) {
-        const uint4 w = codes_bf16(q, b);
-        return mul_bf16(f[0], w, mul_bf16(f[1], w, mul_bf16(f[2], w, d)));
+        // q - 8 itself in bf16: an offset taken off afterwards would cost fp32 sums four of their bits
+        const uint4 h = codes_f16(q, b);
+        float v[8];
+        Vec16<_Float16>::unpack(h, v);
+        const uint4 w = pack16<bf16_t>(v);
+        return mma16<bf16_t>(f[0], w, mma16<bf16_t>(f[1], w, mma16<bf16_t>(f[2], w, d)));
     }
 };
 

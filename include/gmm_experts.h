@@ -31,12 +31,12 @@
  * neither read nor written.  Row strides (ld) are in elements.  Rows are stored in
  * `dtype` (gmm_dtype); products, sums and softmax weights are fp32, each result is
  * rounded once.  Inputs and outputs must not overlap.  Results are bitwise
- * reproducible.  Rows move in 16-byte pieces when the base pointer and the row
- * stride in bytes are multiples of 16 and the width is a multiple of 16 bytes; any
- * other layout takes a slower element-wise path.
+ * reproducible.  Fastest when base pointers, row strides and widths are multiples of
+ * 16 bytes; any other layout goes through slower loads of the same pieces.
  *
  * Limits: 1 <= m <= GMM_MAX_TOPM, 1 <= k <= GMM_MAX_LISTS, 0 <= n with
- * n * m <= 2^30, 1 <= widths <= 2^20, strides <= 2^22; outside them GMM_E_ARG.
+ * n * m <= 2^30, 1 <= widths <= 2^20, strides <= 2^22, and products of no more than 2^24
+ * 128 x 128 tiles; outside them GMM_E_ARG.
  */
 #ifndef GMM_EXPERTS_H
 #define GMM_EXPERTS_H

@@ -141,6 +141,14 @@ def _rows(fn, name, t, rows, width, dtype):
     return ld
 
 
+def _apart(fn, out, *inputs):
+    """An output that starts where an input starts is refused (any other overlap is the caller's to avoid)."""
+    if out is not None and out.data_ptr() != 0:
+        for t in inputs:
+            if t is not None and t.data_ptr() == out.data_ptr():
+                _fail(fn, "an output must not overlap an input")
+
+
 def _code(fn, t):
     code = _CODE.get(t.dtype)
     if code is None:
@@ -212,6 +220,7 @@ def _one_output(fn, lib_fn, routes, src, src_rows, out, out_rows, gamma, stream)
     ld_out = d if out is None else _rows(fn, "out", out, out_rows(n, m), d, src.dtype)
     if gamma is not None:
         _flat(fn, "gamma", gamma, _F32, (n, m))
+    _apart(fn, out, src, gamma)
     tensors = (*routes, src, out, gamma)
     index = _device_of(fn, tensors)
 
@@ -266,6 +275,8 @@ def combine_backward(dout, z, gamma, routes, dz=None, dgamma=None, need=(True, T
     lddz = d if dz is None else _rows(fn, "dz", dz, n * m, d, dout.dtype)
     if dgamma is not None:
         _flat(fn, "dgamma", dgamma, _F32, (n, m))
+    _apart(fn, dz, dout, z, gamma)
+    _apart(fn, dgamma, dout, z, gamma, dz)
     tensors = (*routes, dout, z, gamma, dz, dgamma)
     index = _device_of(fn, tensors)
 
@@ -296,6 +307,7 @@ def linear(x, w, bias, routes, sorted_rows=False, out=None, stream=None):
     if bias is not None:
         _flat(fn, "bias", bias, _F32, (k, do))
     ldy = do if out is None else _rows(fn, "out", out, n * m, do, x.dtype)
+    _apart(fn, out, x, w, bias)
     tensors = (*routes, x, w, bias, out)
     index = _device_of(fn, tensors)
     desc = _CLinear(di, do, ldx, ldy, di, code, 1 if sorted_rows else 0)
@@ -335,6 +347,8 @@ def linear_backward(dy, x, w, routes, sorted_rows=False, dx=None, dw=None, db=No
         _flat(fn, "dw", dw, torch.float32, shape)
     if db is not None:
         _flat(fn, "db", db, _F32, (k, do))
+    for o in (dx, dw, db):
+        _apart(fn, o, dy, x, wt)
     tensors = (*routes, dy, x, wt, dx, dw, db)
     index = _device_of(fn, tensors)
     desc = _CLinear(di, do, ldx, lddy, lddx, code, 1 if sorted_rows else 0)
@@ -402,6 +416,7 @@ def linear4(x, idx, gamma, codes, scales, group=128, bias=None, out=None, stream
     if bias is not None:
         _flat(fn, "bias", bias, _F32, (k, do))
     ldo = do if out is None else _rows(fn, "out", out, n, do, x.dtype)
+    _apart(fn, out, x)
     tensors = (x, idx, gamma, codes, scales, bias, out)
     index = _device_of(fn, tensors)
 

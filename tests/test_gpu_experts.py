@@ -366,6 +366,30 @@ def test_linear4_foreign_components():
     assert np.array_equal(got, np.stack([y[0, 0], np.zeros(do), 2 * y[2, 2], y[3, 3]]))
 
 
+def test_linear4_nonfinite():
+    """A component with a NaN scale and a point with a NaN or an infinity touch only
+    the points that list the one and the rows of the other."""
+    n, m, k, di, do = 12, 2, 5, 256, 40
+    rng = np.random.default_rng(1)
+    for dt in ("f32", "bf16", "f16"):
+        idx = R.assignment(n, m, k, rng)
+        idx[0], idx[1], idx[2] = (3, 4), (0, 1), (2, 0)
+        x = rows_tensor(rng, n, di, R.DT[dt], 0, True)
+        gamma = torch.ones((n, m), device="cuda")
+        codes = dev(rng.integers(0, 256, size=(k, do, di // 2)).astype(np.uint8))
+        scales = torch.ones((k, do, di // 32), dtype=torch.bfloat16, device="cuda")
+        clean = experts.linear4(x, dev(idx), gamma, codes, scales, 32)
+        scales[3, 7, 1] = float("nan")
+        x[1, 5], x[2, 9] = float("nan"), float("inf")
+        got = experts.linear4(x, dev(idx), gamma, codes, scales, 32)
+        hit = (idx == 3).any(1)
+        rows = [p for p in range(n) if p not in (1, 2)]
+        cols = [c for c in range(do) if c != 7]
+        assert torch.equal(got[rows][:, cols], clean[rows][:, cols])
+        assert torch.equal(torch.isnan(got[rows, 7]).cpu(), torch.from_numpy(hit[rows]))
+        assert not torch.isfinite(got[1]).any() and not torch.isfinite(got[2]).any()
+
+
 # --- together -----------------------------------------------------------------------
 @pytest.mark.parametrize("cov,dt", [("diag", "f32"), ("iso", "bf16"), ("full", "f16")])
 def test_mixture_then_models(cov, dt):
@@ -473,6 +497,47 @@ def test_other_stream_and_graph(n):
         assert all(torch.equal(p, q) for p, q in zip(eager, want[1 - turn]))
 
 
+def test_no_points():
+    """n = 0: empty rows, zero gradients of the weights."""
+    r = experts.route(torch.empty((0, 2), dtype=torch.int32, device="cuda"), 3)
+    x, z = torch.empty((0, 16), device="cuda"), torch.empty((0, 24), device="cuda")
+    w, g = torch.ones((3, 24, 16), device="cuda"), torch.empty((0, 2), device="cuda")
+    assert experts.dispatch(x, r).shape == (0, 16) and experts.combine(z, g, r).shape == (0, 24)
+    assert experts.linear(x, w, None, r).shape == (0, 24)
+    dx, dw, db = experts.linear_backward(z, x, w, r)
+    assert dx.shape == (0, 16) and not dw.any() and not db.any()
+    idx = torch.empty((0, 2), dtype=torch.int32, device="cuda")
+    codes, scales = experts.quantize4(w, 32)
+    assert experts.linear4(x, idx, g, codes, scales, 32).shape == (0, 24)
+
+
+def test_offsets_past_32_bits():
+    """Rows whose bytes pass 4 GiB, there and back; every 997th point against its own rows."""
+    n, m, k, d = 9_000_000, 2, 7, 128
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    idx = torch.randint(0, k, (n, m), generator=gen, device="cuda", dtype=torch.int32)
+    x = torch.randint(-3, 4, (n, d), generator=gen, device="cuda").to(torch.bfloat16)
+    gamma = torch.ones((n, m), device="cuda")
+    r = experts.route(idx, k)
+    y = experts.dispatch(x, r)
+    assert y.numel() * y.element_size() > 1 << 32
+    some = torch.cat([torch.arange(0, n, 997, device="cuda"), torch.arange(n - 50, n, device="cuda")])
+    at = r.slot[some].long()
+    assert torch.equal(y[at[:, 0]], x[some]) and torch.equal(y[at[:, 1]], x[some])
+    assert torch.equal(experts.combine(y, gamma, r)[some], 2 * x[some])
+    w = torch.randint(-2, 3, (k, d, d), generator=gen, device="cuda").to(torch.bfloat16)
+    z = experts.linear(x, w, None, r, out=y)
+    ref = torch.stack([x[some].double() @ w[kk].double().t().contiguous() for kk in range(k)])
+    for i in range(m):
+        want = ref[idx[some, i].long(), torch.arange(len(some), device="cuda")]
+        assert torch.equal(z[at[:, i]], want.to(torch.bfloat16))
+    dx = experts.linear_backward(z, None, w, r, need=(True, False, False))[0]
+    want = torch.stack([z[at[:, 0]].double() @ w[kk].double() for kk in range(k)])
+    want = want[idx[some, 0].long(), torch.arange(len(some), device="cuda")]
+    # 128 products of whole numbers, at most 768 x 2 each: exact in fp32
+    assert torch.equal(dx[at[:, 0]], want.to(torch.bfloat16))
+
+
 def test_refused_tensors():
     """Wrong types, shapes, strides and devices are refused before anything runs."""
     x, idx, gamma, w, b, dout, codes, scales, k = _inputs(10, 2, 3, 16, 24, "f32", 1)
@@ -489,6 +554,7 @@ def test_refused_tensors():
         lambda: experts.linear_backward(y, x, w, r, need=(True, False, True)),
         lambda: experts.linear_backward(y[:5], x, w, r),
         lambda: experts.combine_backward(dout, None, gamma, r),
+        lambda: experts.combine_backward(dout, y, gamma, r, dz=y), lambda: experts.linear(x, w, b, r, out=x),
         lambda: experts.linear4(x, idx, gamma, codes, scales, 48), lambda: experts.linear4(x, idx, gamma, codes, scales, 16),
         lambda: experts.linear4(x, idx, gamma, codes[:, :, :3], scales, 32),
     ]

@@ -8,17 +8,25 @@
 //
 // A workgroup computes a tile of 64 x 64 blocks, one a wave, each as 2 x 2 blocks of
 // v_mfma_f32_32x32x16 (16-bit storage) or v_mfma_f32_32x32x2_f32, fp32 accumulators.  Operand
-// tiles go through LDS in 16-byte pieces, 128 bytes of the contraction (64 or 32
-// elements) a step, two buffers: the pieces of step i + 1 are fetched while step i is
-// multiplied, straight into LDS (global_load_lds) where rows allow 16-byte pieces, through
+// tiles go through LDS in 16-byte pieces, 64 or 128 bytes of the contraction a step,
+// two or three steps at a time: the pieces of the next steps are fetched while one is multiplied,
+// straight into LDS (global_load_lds) where rows allow 16-byte pieces, through
 // registers where they do not.  An operand contiguous along the contraction is
-// kept [row][128 bytes], its pieces XOR-swizzled by the row, and read a fragment (8 or 4
+// kept [row][step], its pieces XOR-swizzled by the row, and read a fragment (8 or 4
 // elements) at a time; one that is contiguous along the output is kept
 // [contraction][columns] and read with ds_read_b64_tr_b16 (16-bit) or element by
 // element (fp32).  Pieces beyond a row's end, a list's end or the contraction come
 // from 16 zero bytes, so they add nothing.
 //
+// Measured (bf16): 32768 rows in 8 lists, 1024 -> 2048: forward 143 us (960 TFLOP/s), dx 136
+// (1010), dw 173 (795); in 64 lists 201, 187, 269: the weights' 268 MB and their gradient's 537 MB
+// pass the memory too.  Bound there by LDS reads and the barrier of each step; 2e6 rows in 256 lists, 128 -> 128, fp16,
+// 225 us: bound by the memory, where the gathered rows pass twice (a point's two lists
+// lie far apart).  fp32 is bound by its products (a sixteenth of the 16-bit rate) and, on short chunks, by latency.
+//
 // Workgroup -> rows: find_rows (experts_internal.h); the host never learns the lists' lengths.
+
+#include <type_traits>
 
 #include "experts_internal.h"
 
@@ -70,16 +78,15 @@ template <> __device__ __forceinline__ f32x16 mma<float>(const uint4& a, const u
     return __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.w), __uint_as_float(b.w), c, 0, 0, 0);
 }
 
-// A fragment of a 32 x 32 block has rows 0-15 in the even and rows 16-31 in the odd
-// groups of 16 lanes; taken as the second operand of a 16 x 16 product against
-// this first one (row 0: ones in the even groups, row 1: ones in the odd ones), row 0 and
-// row 1 of the product are the sums of the fragment's rows over the contraction.
-template <typename T> __device__ __forceinline__ uint4 row_sums() {
-    const int lane = threadIdx.x & 63;
-    T one[Vec16<T>::kElems];
+// Sum of the elements a lane holds of a fragment: half of the contraction of row lane % 32.
+template <typename T> __device__ __forceinline__ float add_elements(const uint4& frag) {
+    float v[Vec16<T>::kElems];
+    Vec16<T>::unpack(frag, v);
 #pragma unroll
-    for (int i = 0; i < Vec16<T>::kElems; ++i) from_f32((lane & 15) == (lane >> 4 & 1) ? 1.0f : 0.0f, one + i);
-    return __builtin_bit_cast(uint4, one);
+    for (int w = Vec16<T>::kElems / 2; w > 0; w >>= 1)
+#pragma unroll
+        for (int i = 0; i < w; ++i) v[i] += v[i + w];
+    return v[0];
 }
 
 // Four consecutive outputs of a row from column c on.
@@ -176,9 +183,12 @@ __device__ __forceinline__ int tile_of(int block, int tiles) {
     return (block & 7) * per + (block >> 3);
 }
 
-// y = x W^T + b (BACK false) or dx = dy W (BACK true) on one tile.
-template <typename T, bool VEC, bool BACK, typename S>
+// y = x W^T + b (BACK false) or dx = dy W (BACK true) on one tile.  VIN: rows along d_in (x, W, dx) are whole
+// aligned pieces; VOUT: rows along d_out (y, dy) are.  An operand whose rows are not goes through registers,
+// one step ahead; a result whose rows are not leaves from the accumulators.
+template <typename T, bool VIN, bool VOUT, bool BACK, typename S>
 __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear(const LinArgs a) {
+    constexpr bool AV = BACK ? VOUT : VIN, BV = VIN, CV = BACK ? VIN : VOUT;   // the operands' and the result's rows
     constexpr int WM = S::WM, kStep = S::kStep, kStages = S::kStages, kFrags = S::kFrags;
     using RT = RowTile<kStep>;
     using CT = ColTile<T, S::kN, kStep>;
@@ -217,7 +227,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear(const 
         const int s = lr.s0 + RA * (wave * AJ + j) + lane / PA;
         const int row = a.gather ? source_row(e[j], a.magic, a.rows) : s;
         there_a[j] = s < lr.s1 && row >= 0;
-        pa[j] = there_a[j] ? (const char*)((const T*)a.a + (int64_t)row * a.lda + (VEC ? ca : 0)) : zero;
+        pa[j] = there_a[j] ? (const char*)((const T*)a.a + (int64_t)row * a.lda + (AV ? ca : 0)) : zero;
         sa[j] = there_a[j] ? kStep : 0;
     }
     constexpr int RI = 64 / CT::kPieces;   // BACK: tile rows of a wave load
@@ -226,67 +236,66 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear(const 
         if constexpr (!BACK) {
             const int r = n0 + RA * (wave * BJ + j) + lane / PA;
             there_b[j] = r < n1;
-            pb[j] = there_b[j] ? (const char*)(w + (int64_t)r * kd + (VEC ? ca : 0)) : zero;
+            pb[j] = there_b[j] ? (const char*)(w + (int64_t)r * kd + (BV ? ca : 0)) : zero;
             sb[j] = there_b[j] ? kStep : 0;
             rb[j] = 0;
         } else {
             rb[j] = (wave * BJ + j) * RI + lane / CT::kPieces;
             const int c = n0 + ((lane % CT::kPieces) ^ CT::swz(rb[j])) * E;
             there_b[j] = c < n1;
-            pb[j] = there_b[j] ? (const char*)(w + (int64_t)rb[j] * nd + (VEC ? c : 0)) : zero;
+            pb[j] = there_b[j] ? (const char*)(w + (int64_t)rb[j] * nd + (BV ? c : 0)) : zero;
             sb[j] = there_b[j] ? (int64_t)KS * nd * (int)sizeof(T) : 0;
         }
     }
     const uint32_t base = lds_address(lds);
-    Loose ra[VEC ? 1 : AJ], rb_[VEC ? 1 : BJ];
-    // the pieces of the step at k0, the next one not yet fetched: VEC into buffer `buf`, else into registers
+    Loose ra[AV ? 1 : AJ], rl[BV ? 1 : BJ];
+    // the pieces of the step at k0, the next one not yet fetched: into buffer `buf` or into registers
     auto fetch = [&](int k0, int buf) {
-        if constexpr (VEC) {
-            const uint32_t to = base + buf * kStage;
-            const bool whole = k0 + KS <= kd;
+        const uint32_t to = base + buf * kStage;
+        const bool whole = k0 + KS <= kd;
 #pragma unroll
-            for (int j = 0; j < AJ; ++j) {
+        for (int j = 0; j < AJ; ++j) {
+            if constexpr (AV) {
                 fetch_piece(whole || k0 + ca < kd ? pa[j] : zero, to + (wave * AJ + j) * 1024);
                 pa[j] += sa[j];
-            }
-#pragma unroll
-            for (int j = 0; j < BJ; ++j) {
-                fetch_piece(whole || k0 + (BACK ? rb[j] : ca) < kd ? pb[j] : zero, to + S::kABytes + (wave * BJ + j) * 1024);
-                pb[j] += sb[j];
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < AJ; ++j)
+            } else {
                 ra[j] = load_piece<T>((const T*)pa[j], there_a[j], k0 + ca, kd, zero);
-#pragma unroll
-            for (int j = 0; j < BJ; ++j) {
-                if constexpr (BACK) {
-                    const int c = n0 + ((lane % CT::kPieces) ^ CT::swz(rb[j])) * E;
-                    rb_[j] = load_piece<T>((const T*)pb[j], there_b[j] && k0 + rb[j] < kd, c, nd, zero);
-                    pb[j] += sb[j];
-                } else {
-                    rb_[j] = load_piece<T>((const T*)pb[j], there_b[j], k0 + ca, kd, zero);
-                }
             }
         }
+#pragma unroll
+        for (int j = 0; j < BJ; ++j) {
+            if constexpr (BV) {
+                fetch_piece(whole || k0 + (BACK ? rb[j] : ca) < kd ? pb[j] : zero, to + S::kABytes + (wave * BJ + j) * 1024);
+            } else if constexpr (BACK) {
+                const int c = n0 + ((lane % CT::kPieces) ^ CT::swz(rb[j])) * E;
+                rl[j] = load_piece<T>((const T*)pb[j], there_b[j] && k0 + rb[j] < kd, c, nd, zero);
+            } else {
+                rl[j] = load_piece<T>((const T*)pb[j], there_b[j], k0 + ca, kd, zero);
+            }
+            if (BV || BACK) pb[j] += sb[j];
+        }
     };
-    auto put = [&](int buf) {
+    auto put = [&](int buf) {   // what came into registers
         char* to = lds + buf * kStage + lane * 16;
+        if constexpr (!AV) {
 #pragma unroll
-        for (int j = 0; j < AJ; ++j) *(uint4*)(to + (wave * AJ + j) * 1024) = settle(ra[j]);
+            for (int j = 0; j < AJ; ++j) *(uint4*)(to + (wave * AJ + j) * 1024) = settle(ra[j]);
+        }
+        if constexpr (!BV) {
 #pragma unroll
-        for (int j = 0; j < BJ; ++j) *(uint4*)(to + S::kABytes + (wave * BJ + j) * 1024) = settle(rb_[j]);
+            for (int j = 0; j < BJ; ++j) *(uint4*)(to + S::kABytes + (wave * BJ + j) * 1024) = settle(rl[j]);
+        }
     };
 
     // blocks of columns with outputs (16-bit pieces: not worth the branches)
-    constexpr bool kAll = VEC && sizeof(T) == 2;
+    constexpr bool kAll = AV && BV && sizeof(T) == 2;
     const bool live[2] = {kAll || n0 + wn < n1, kAll || n0 + wn + 32 < n1};
     f32x16 acc[2][2] = {};
     if (!BACK && a.bias != nullptr) {   // sums start from the bias
         const float* bias = a.bias + (int64_t)lr.k * nd;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            if constexpr (VEC) {
+            if constexpr (CV) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int c = n0 + wn + 32 * h + 8 * q + 4 * (lane >> 5);
@@ -302,17 +311,14 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear(const 
             }
     }
     const int steps = (kd + KS - 1) / KS;
-    constexpr int kAhead = VEC ? kStages - 1 : 1;   // steps on their way (registers hold one)
+    constexpr int kAhead = AV && BV ? kStages - 1 : 1;   // steps on their way (registers hold one)
     for (int i = 0; i < kAhead && i < steps; ++i) fetch(i * KS, i);
     int buf = 0;
     for (int i = 0; i < steps; ++i) {
         // this step's pieces are in LDS, and every wave has read the last step's
-        if constexpr (VEC) {
-            if (i + kAhead - 1 < steps) wait_pieces<(kAhead - 1) * (AJ + BJ)>();
-            else wait_pieces<0>();
-        } else {
-            put(buf);
-        }
+        if (kAhead > 1 && i + kAhead - 1 < steps) wait_pieces<(kAhead - 1) * (AJ + BJ)>();
+        else if (AV || BV) wait_pieces<0>();
+        put(buf);
         __syncthreads();
         if (i + kAhead < steps) fetch((i + kAhead) * KS, buf + kAhead < kStages ? buf + kAhead : buf + kAhead - kStages);
         const char* ta = lds + buf * kStage;
@@ -329,14 +335,14 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear(const 
             for (int h = 0; h < 2; ++h)
                 if (live[h]) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)   // VEC: lanes along the slots, else along the columns
-                        acc[i][h] = VEC ? mma<T>(fb[h], fa[i], acc[i][h]) : mma<T>(fa[i], fb[h], acc[i][h]);
+                    for (int i = 0; i < 2; ++i)   // CV: lanes along the slots, else along the columns
+                        acc[i][h] = CV ? mma<T>(fb[h], fa[i], acc[i][h]) : mma<T>(fa[i], fb[h], acc[i][h]);
                 }
         }
         buf = buf + 1 < kStages ? buf + 1 : 0;
     }
 
-    if constexpr (VEC) {
+    if constexpr (CV) {
         // lane: slot lane % 32, four consecutive outputs per register group;
         // through LDS, so that a row leaves in whole pieces: the wave's 64 x 64 block, two halves of
         // 32 rows, pieces swizzled by the row
@@ -398,7 +404,7 @@ constexpr int kFewRows = 16, kFewOutputs = 16, kFewWaves = 4;
 // y = x W^T + b on 16 outputs of up to 16 rows of a list: nothing to share between
 // workgroups, so no LDS tiles.  The waves split the contraction, every lane streams its row of
 // W_k and of x into 16 x 16 products, and the four partial blocks are summed in order.
-template <typename T, bool VEC>
+template <typename T, bool VIN, bool VOUT>
 __global__ __launch_bounds__(64 * kFewWaves) void k_linear_few(const LinArgs a) {
     constexpr int E = Vec16<T>::kElems, KS = 4 * E;   // contraction of a product
     constexpr int kAhead = 4;                         // products whose pieces are in flight
@@ -420,7 +426,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_linear_few(const LinArgs a) 
     const int mine = (lane >> 4) * E;
     const char* zero = zero_address();
     auto piece = [&](const T* p, bool there, int k) {
-        if constexpr (VEC) return Loose{*(const uint4*)(there && k < a.d_in ? (const char*)(p + k) : zero), 0};
+        if constexpr (VIN) return Loose{*(const uint4*)(there && k < a.d_in ? (const char*)(p + k) : zero), 0};
         else return load_piece<T>(p, there, k, a.d_in, zero);
     };
     for (int k0 = wave * KS; k0 < a.d_in; k0 += kAhead * kFewWaves * KS) {
@@ -432,7 +438,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_linear_few(const LinArgs a) 
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
-            acc = VEC ? mma16<T>(fw[u].v, fx[u].v, acc) : mma16<T>(settle(fw[u]), settle(fx[u]), acc);
+            acc = VIN ? mma16<T>(fw[u].v, fx[u].v, acc) : mma16<T>(settle(fw[u]), settle(fx[u]), acc);
     }
     part[wave][lane] = acc;
     __syncthreads();
@@ -446,7 +452,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_linear_few(const LinArgs a) 
         for (int q = 1; q < kFewWaves; ++q) v[e] += part[q][lane][e];
         if (a.bias != nullptr) v[e] += a.bias[(int64_t)lr.k * a.d_out + min(c + e, a.d_out - 1)];
     }
-    store4<T, VEC>((T*)a.c + (int64_t)s * a.ldc, c, a.d_out, v);
+    store4<T, VOUT>((T*)a.c + (int64_t)s * a.ldc, c, a.d_out, v);
 }
 
 // ---- gradient of the weights
@@ -475,7 +481,7 @@ struct GradArgs {
 __device__ __host__ __forceinline__ int64_t first_slot(int64_t a, int chunk) { return 2 * a / chunk; }
 
 // dW (and db) over one chunk of one list, one tile: 64 WM of d_in x 64 WN of d_out.
-template <typename T, bool VEC, typename S>
+template <typename T, bool VIN, bool VOUT, typename S>
 __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear_dw(const GradArgs a) {
     constexpr int WM = S::WM, kStages = S::kStages, kFrags = S::kFrags;
     using XT = ColTile<T, S::kM, S::kStep>;
@@ -503,7 +509,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear_dw(con
     const bool with_db = a.db != nullptr && i0 == 0 && wi == 0;
 
     const uint32_t base = lds_address(lds);
-    Loose rx[VEC ? 1 : XJ], ry[VEC ? 1 : YJ];
+    Loose rx[VIN ? 1 : XJ], ry[VOUT ? 1 : YJ];
     // Rows of x behind the slots, one slot a thread and segment of kThreads slots, two segments in
     // LDS: an entry loaded in every step would be waited for behind the pieces on their way.
     constexpr int R = S::kThreads, SPR = R / KS;   // slots, steps of a segment
@@ -531,7 +537,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear_dw(con
         rowy[j] = lr.s0 + (wave * YJ + j) * YR + lane / YT::kPieces;
         cy[j] = o0 + ((lane % YT::kPieces) ^ YT::swz((wave * YJ + j) * YR + lane / YT::kPieces)) * E;
         const bool there = cy[j] < o1;
-        py[j] = there ? (const char*)((const T*)a.dy + (int64_t)rowy[j] * a.ldy + (VEC ? cy[j] : 0)) : zero;
+        py[j] = there ? (const char*)((const T*)a.dy + (int64_t)rowy[j] * a.ldy + (VOUT ? cy[j] : 0)) : zero;
         sy[j] = there ? (int64_t)KS * a.ldy * (int)sizeof(T) : 0;
     }
     // the step at slot s0, the next one not yet fetched; its rows of x are in from[]
@@ -543,44 +549,44 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear_dw(con
             const int from = source[(s0 - lr.s0 + (wave * XJ + j) * XR + lane / XT::kPieces) & (2 * R - 1)];
             const bool there = from >= 0 && cx[j] < i1;
             const char* row = (const char*)((const T*)a.x + (int64_t)from * a.ldx);
-            if constexpr (VEC) fetch_piece(there ? row + cx[j] * (int)sizeof(T) : zero, to + (wave * XJ + j) * 1024);
+            if constexpr (VIN) fetch_piece(there ? row + cx[j] * (int)sizeof(T) : zero, to + (wave * XJ + j) * 1024);
             else rx[j] = load_piece<T>((const T*)row, there, cx[j], a.d_in, zero);
         }
 #pragma unroll
         for (int j = 0; j < YJ; ++j) {
             const bool there = whole || s0 - lr.s0 + rowy[j] < s1;
-            if constexpr (VEC) fetch_piece(there ? py[j] : zero, to + S::kABytes + (wave * YJ + j) * 1024);
+            if constexpr (VOUT) fetch_piece(there ? py[j] : zero, to + S::kABytes + (wave * YJ + j) * 1024);
             else ry[j] = load_piece<T>((const T*)py[j], there, cy[j], a.d_out, zero);
             py[j] += sy[j];
         }
     };
-    auto put = [&](int buf) {
+    auto put = [&](int buf) {   // what came into registers
         char* to = lds + buf * kStage + lane * 16;
+        if constexpr (!VIN) {
 #pragma unroll
-        for (int j = 0; j < XJ; ++j) *(uint4*)(to + (wave * XJ + j) * 1024) = settle(rx[j]);
+            for (int j = 0; j < XJ; ++j) *(uint4*)(to + (wave * XJ + j) * 1024) = settle(rx[j]);
+        }
+        if constexpr (!VOUT) {
 #pragma unroll
-        for (int j = 0; j < YJ; ++j) *(uint4*)(to + S::kABytes + (wave * YJ + j) * 1024) = settle(ry[j]);
+            for (int j = 0; j < YJ; ++j) *(uint4*)(to + S::kABytes + (wave * YJ + j) * 1024) = settle(ry[j]);
+        }
     };
 
     // blocks with gradients (16-bit pieces: not worth the branches)
-    constexpr bool kAll = VEC && sizeof(T) == 2;
+    constexpr bool kAll = VIN && VOUT && sizeof(T) == 2;
     const bool live[2] = {kAll || i0 + wi < i1, kAll || i0 + wi + 32 < i1};
     const bool live_o[2] = {kAll || o0 + wo < o1, kAll || o0 + wo + 32 < o1};
     f32x16 acc[2][2] = {};
-    f32x4 sum[2] = {};
-    const uint4 ones = row_sums<T>();
+    float sum[2] = {};
     const int steps = (s1 - lr.s0 + KS - 1) / KS;
-    constexpr int kAhead = VEC ? kStages - 1 : 1;
+    constexpr int kAhead = VIN && VOUT ? kStages - 1 : 1;
     for (int i = 0; i < kAhead && i < steps; ++i) fetch(lr.s0 + i * KS, i);
     int buf = 0, next = -1;   // next: the entry of this thread's slot in the segment after the one being fetched
     static_assert(SPR - 3 >= kAhead && (R & (R - 1)) == 0, "a segment is loaded and kept while its forerunner is fetched");
     for (int i = 0; i < steps; ++i) {
-        if constexpr (VEC) {
-            if (i + kAhead - 1 < steps) wait_pieces<(kAhead - 1) * (XJ + YJ)>();
-            else wait_pieces<0>();
-        } else {
-            put(buf);
-        }
+        if (kAhead > 1 && i + kAhead - 1 < steps) wait_pieces<(kAhead - 1) * (XJ + YJ)>();
+        else if (VIN || VOUT) wait_pieces<0>();
+        put(buf);
         // the last step of a segment is about to be fetched: every wave is past the segment before it
         const int f = i + kAhead;
         if (f % SPR == SPR - 1) keep(f / SPR + 1, next);
@@ -606,7 +612,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear_dw(con
                     if (live[i] && live_o[h]) acc[i][h] = mma<T>(fy[h], fx[i], acc[i][h]);
             if (with_db) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) sum[h] = mma16<T>(ones, fy[h], sum[h]);
+                for (int h = 0; h < 2; ++h) sum[h] += add_elements<T>(fy[h]);
             }
         }
         buf = buf + 1 < kStages ? buf + 1 : 0;
@@ -620,12 +626,13 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear_dw(con
         dw = a.part + slot * ((int64_t)a.d_out * a.d_in + a.d_out);
         db = with_db ? dw + (int64_t)a.d_out * a.d_in : nullptr;
     }
-    if (with_db && lane < 16) {
+    if (with_db) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-                if (o0 + wo + 32 * h + 16 * r + lane < o1) db[o0 + wo + 32 * h + 16 * r + lane] = sum[h][r];
+        for (int h = 0; h < 2; ++h) {
+            const float all = halves_sum(sum[h]);
+            const int o = o0 + wo + 32 * h + (lane & 31);
+            if (lane < 32 && o < o1) db[o] = all;
+        }
     }
     // lane: input i = lane % 32, so that a register's store covers 128 bytes of two rows; outputs
     // 8 (r / 4) + 4 (lane / 32) + r % 4
@@ -711,7 +718,7 @@ gmm_status grid_of(int64_t tiles, int* grid) {
     return GMM_OK;
 }
 
-template <typename T, bool VEC, bool BACK, typename S>
+template <typename T, bool VIN, bool VOUT, bool BACK, typename S>
 gmm_status launch_shape(const LinArgs& a, hipStream_t stream) {
     LinArgs b = a;
     int grid;
@@ -721,18 +728,18 @@ gmm_status launch_shape(const LinArgs& a, hipStream_t stream) {
     b.col_step = step_of(nd, S::kN);
     const gmm_status st = grid_of((int64_t)b.row_blocks * b.col_blocks, &grid);
     if (st != GMM_OK) return st;
-    hipLaunchKernelGGL((k_linear<T, VEC, BACK, S>), dim3(grid), dim3(S::kThreads), 0, stream, b);
+    hipLaunchKernelGGL((k_linear<T, VIN, VOUT, BACK, S>), dim3(grid), dim3(S::kThreads), 0, stream, b);
     return launched();
 }
 
-template <typename T, bool VEC> gmm_status launch_few(const LinArgs& a, hipStream_t stream) {
+template <typename T, bool VIN, bool VOUT> gmm_status launch_few(const LinArgs& a, hipStream_t stream) {
     LinArgs b = a;
     int grid;
     b.row_blocks = (int)row_blocks(a.rows, a.K, kFewRows, &b.by_slot);
     b.col_blocks = blocks_of(a.d_out, kFewOutputs);
     const gmm_status st = grid_of((int64_t)b.row_blocks * b.col_blocks, &grid);
     if (st != GMM_OK) return st;
-    hipLaunchKernelGGL((k_linear_few<T, VEC>), dim3(b.row_blocks * b.col_blocks), dim3(64 * kFewWaves), 0, stream, b);
+    hipLaunchKernelGGL((k_linear_few<T, VIN, VOUT>), dim3(b.row_blocks * b.col_blocks), dim3(64 * kFewWaves), 0, stream, b);
     return launched();
 }
 
@@ -756,28 +763,29 @@ bool large_tiles(const LinArgs& a, int kd, int nd) {
 // 256 lists of 4, 1024 -> 256: 28 / 30, of 16: 50 / 31).
 bool few_rows(const LinArgs& a) { return a.rows <= 4 * (int64_t)a.K || a.rows <= 128; }
 
-template <typename T, bool VEC, bool BACK> gmm_status launch_linear(const LinArgs& a, hipStream_t stream) {
+template <typename T, bool VIN, bool VOUT, bool BACK> gmm_status launch_linear(const LinArgs& a, hipStream_t stream) {
     if constexpr (!BACK)
-        if (few_rows(a)) return launch_few<T, VEC>(a, stream);
-    if constexpr (VEC && sizeof(T) == 2)
+        if (few_rows(a)) return launch_few<T, VIN, VOUT>(a, stream);
+    if constexpr (VIN && VOUT && sizeof(T) == 2)
         if (large_tiles(a, BACK ? a.d_out : a.d_in, BACK ? a.d_in : a.d_out))
-            return launch_shape<T, VEC, BACK, Large>(a, stream);
-    return launch_shape<T, VEC, BACK, Small>(a, stream);
+            return launch_shape<T, VIN, VOUT, BACK, Large>(a, stream);
+    return launch_shape<T, VIN, VOUT, BACK, Small>(a, stream);
 }
 
-template <bool BACK> gmm_status run_linear(const LinArgs& a, int dtype, bool vec, hipStream_t stream) {
+template <bool BACK, typename T> gmm_status linear_of(const LinArgs& a, bool vin, bool vout, hipStream_t stream) {
+    if (vin) return vout ? launch_linear<T, true, true, BACK>(a, stream) : launch_linear<T, true, false, BACK>(a, stream);
+    return vout ? launch_linear<T, false, true, BACK>(a, stream) : launch_linear<T, false, false, BACK>(a, stream);
+}
+
+template <bool BACK> gmm_status run_linear(const LinArgs& a, int dtype, bool vin, bool vout, hipStream_t stream) {
     switch (dtype) {
-        case GMM_F32:
-            return vec ? launch_linear<float, true, BACK>(a, stream) : launch_linear<float, false, BACK>(a, stream);
-        case GMM_BF16:
-            return vec ? launch_linear<bf16_t, true, BACK>(a, stream) : launch_linear<bf16_t, false, BACK>(a, stream);
-        default:
-            return vec ? launch_linear<_Float16, true, BACK>(a, stream)
-                       : launch_linear<_Float16, false, BACK>(a, stream);
+        case GMM_F32: return linear_of<BACK, float>(a, vin, vout, stream);
+        case GMM_BF16: return linear_of<BACK, bf16_t>(a, vin, vout, stream);
+        default: return linear_of<BACK, _Float16>(a, vin, vout, stream);
     }
 }
 
-template <typename T, bool VEC, typename S> gmm_status launch_dw_shape(const GradArgs& a, hipStream_t stream) {
+template <typename T, bool VIN, bool VOUT, typename S> gmm_status launch_dw_shape(const GradArgs& a, hipStream_t stream) {
     GradArgs b = a;
     int grid;
     b.row_blocks = (int)row_blocks(a.rows, a.K, a.chunk, &b.by_slot);
@@ -786,7 +794,7 @@ template <typename T, bool VEC, typename S> gmm_status launch_dw_shape(const Gra
     const int64_t per = (int64_t)b.in_blocks * b.out_blocks;
     const gmm_status st = grid_of(b.row_blocks * (per < 8 ? per : (per + 7) / 8 * 8), &grid);
     if (st != GMM_OK) return st;
-    hipLaunchKernelGGL((k_linear_dw<T, VEC, S>), dim3(grid), dim3(S::kThreads), 0, stream, b);
+    hipLaunchKernelGGL((k_linear_dw<T, VIN, VOUT, S>), dim3(grid), dim3(S::kThreads), 0, stream, b);
     return launched();
 }
 
@@ -798,16 +806,25 @@ bool large_grad(const GradArgs& a) {
     return a.d_in >= 256 && a.d_out >= 256 && a.rows >= 512 * (int64_t)a.K && (a.rows / a.chunk + a.K) * tiles >= 256;
 }
 
-template <typename T, bool VEC> gmm_status launch_dw(const GradArgs& a, hipStream_t stream) {
+// Large tiles exist for whole 16-bit rows.
+template <typename T, bool VEC> struct GradShape {
+    using L = typename std::conditional<VEC && sizeof(T) == 2, LargeGrad, Small>::type;
+};
+
+template <typename T, bool VIN, bool VOUT> gmm_status launch_dw(const GradArgs& a, hipStream_t stream) {
     gmm_status st;
-    if constexpr (VEC && sizeof(T) == 2)
-        st = large_grad(a) ? launch_dw_shape<T, VEC, LargeGrad>(a, stream) : launch_dw_shape<T, VEC, Small>(a, stream);
-    else st = launch_dw_shape<T, VEC, Small>(a, stream);
+    if (VIN && VOUT && sizeof(T) == 2 && large_grad(a)) st = launch_dw_shape<T, VIN, VOUT, typename GradShape<T, VIN && VOUT>::L>(a, stream);
+    else st = launch_dw_shape<T, VIN, VOUT, Small>(a, stream);
     if (st != GMM_OK) return st;
     const int64_t wide = (int64_t)a.d_out * a.d_in;
     const int64_t parts = (wide + a.d_out + 255) / 256;
     hipLaunchKernelGGL(k_linear_dw_join, dim3(parts < 256 ? parts : 256, a.K), dim3(256), 0, stream, a);
     return launched();
+}
+
+template <typename T> gmm_status dw_of(const GradArgs& a, bool vin, bool vout, hipStream_t stream) {
+    if (vin) return vout ? launch_dw<T, true, true>(a, stream) : launch_dw<T, true, false>(a, stream);
+    return vout ? launch_dw<T, false, true>(a, stream) : launch_dw<T, false, false>(a, stream);
 }
 
 }  // namespace
@@ -830,9 +847,9 @@ gmm_status gmm_linear(const gmm_routes* routes, const gmm_linear_desc* desc, con
     LinArgs a = {routes->offsets, routes->entry, (int)(routes->n * routes->m), routes->k, magic_of(routes->m), false,
                  desc->sorted_rows == 0, x, desc->ldx, w, (int)desc->d_in, (int)desc->d_out, bias, y, desc->ldy, 0, 0, 0};
     const int es = elem_size(desc->dtype);
-    const bool vec = desc->d_in * es % 16 == 0 && desc->ldx * es % 16 == 0 && aligned16(x) && aligned16(w) &&
-                     desc->d_out * es % 16 == 0 && desc->ldy * es % 16 == 0 && aligned16(y);
-    return run_linear<false>(a, desc->dtype, vec, stream);
+    const bool vin = desc->d_in * es % 16 == 0 && desc->ldx * es % 16 == 0 && aligned16(x) && aligned16(w);
+    const bool vout = desc->d_out * es % 16 == 0 && desc->ldy * es % 16 == 0 && aligned16(y);
+    return run_linear<false>(a, desc->dtype, vin, vout, stream);
 }
 
 gmm_status gmm_linear_backward_workspace_bytes(int64_t n, int32_t m, int32_t k, const gmm_linear_desc* desc,
@@ -868,13 +885,13 @@ gmm_status gmm_linear_backward(const gmm_routes* routes, const gmm_linear_desc* 
         if (ws_bytes < need) return GMM_E_WORKSPACE;
     }
     const int es = elem_size(desc->dtype);
-    const bool wide = desc->d_in * es % 16 == 0 && desc->d_out * es % 16 == 0;
-    const bool dy_vec = desc->ldy * es % 16 == 0 && aligned16(dy);
+    const bool whole_in = desc->d_in * es % 16 == 0;
+    const bool vout = desc->d_out * es % 16 == 0 && desc->ldy * es % 16 == 0 && aligned16(dy);
     if (dx != nullptr && rows > 0) {
         LinArgs a = {routes->offsets, routes->entry, (int)rows, routes->k, magic_of(routes->m), false, false, dy,
                      desc->ldy, w, (int)desc->d_in, (int)desc->d_out, nullptr, dx, desc->lddx, 0, 0, 0};
-        const bool vec = wide && dy_vec && aligned16(w) && desc->lddx * es % 16 == 0 && aligned16(dx);
-        if ((st = run_linear<true>(a, desc->dtype, vec, stream)) != GMM_OK) return st;
+        const bool vin = whole_in && aligned16(w) && desc->lddx * es % 16 == 0 && aligned16(dx);
+        if ((st = run_linear<true>(a, desc->dtype, vin, vout, stream)) != GMM_OK) return st;
     }
     if (dw == nullptr) return GMM_OK;
     if (rows == 0) {   // every list is empty
@@ -886,11 +903,11 @@ gmm_status gmm_linear_backward(const gmm_routes* routes, const gmm_linear_desc* 
     GradArgs g = {routes->offsets, routes->entry, (int)rows, routes->k, magic_of(routes->m), false,
                   desc->sorted_rows == 0, chunk_rows(rows, desc), x, desc->ldx, dy, desc->ldy, (int)desc->d_in,
                   (int)desc->d_out, dw, db, (float*)ws, 0, 0, 0, 0, 0};
-    const bool vec = wide && dy_vec && desc->ldx * es % 16 == 0 && aligned16(x) && aligned16(dw);
+    const bool vin = whole_in && desc->ldx * es % 16 == 0 && aligned16(x);
     switch (desc->dtype) {
-        case GMM_F32: return vec ? launch_dw<float, true>(g, stream) : launch_dw<float, false>(g, stream);
-        case GMM_BF16: return vec ? launch_dw<bf16_t, true>(g, stream) : launch_dw<bf16_t, false>(g, stream);
-        default: return vec ? launch_dw<_Float16, true>(g, stream) : launch_dw<_Float16, false>(g, stream);
+        case GMM_F32: return dw_of<float>(g, vin, vout, stream);
+        case GMM_BF16: return dw_of<bf16_t>(g, vin, vout, stream);
+        default: return dw_of<_Float16>(g, vin, vout, stream);
     }
 }
 

@@ -17,6 +17,13 @@
 // 0x4300 | q is 128 + q, and a second product with -136 takes the offset off.  fp32 rows are
 // split into three bf16 parts, which hold all 24 bits, and meet q - 8 in bf16.
 
+//
+// Measured: one point in two of 16 models 4096 -> 4096 (bf16, groups of 128) 8.4 us, 17 MB of codes; 24
+// points in four of 64 models 1024 -> 2048 (fp16, groups of 64) 33 us.  Lanes that hold different rows
+// of weights load from different lines, 64 cycles an instruction; so codes and x come into LDS row by
+// row, and the scales are staged there for all components of a phase: with loads straight into the
+// operands' registers the batch took 51 us, 20 of them for the scales.
+
 #include <type_traits>
 
 #include "experts_internal.h"
@@ -424,7 +431,8 @@ template <typename T, bool VEC> gmm_status launch_linear4(const Lin4Args& a, int
         else if (group == 64) go(k_linear4<T, VEC, 64, P>);
         else go(k_linear4<T, VEC, 128, P>);
     };
-    // the widest pieces that still give every wave a piece of some component: each costs a component's
+    // the widest pieces that still give every wave a piece of some component (us at 512 / 256 / 128 columns:
+    // one point, two models 4096 -> 4096: 8.4 / 9.7 / 12.4; 24 points, 1024 -> 2048: 33 / 32 / 38): each costs a component's
     // bookkeeping once (fp32's three parts of x fill the registers at 256)
     const int listed = (a.n < b.points ? a.n : b.points) * a.m;
     auto fills = [&](int piece) { return (int64_t)((a.d_in + piece - 1) / piece) * listed >= kWaves; };

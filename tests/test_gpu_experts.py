@@ -244,12 +244,15 @@ def test_linear_nonfinite_rows(dt):
     x = rows_tensor(rng, n, d, t, 0, True)
     w = rows_tensor(rng, k * d, d, t, 0, True).reshape(k, d, d).contiguous()
     dy = rows_tensor(rng, n * m, d, t, 0, True)
-    clean = experts.linear(x, w, None, r), *experts.linear_backward(dy, x, w, r)[:2]
+    clean = experts.linear(x, w, None, r), *experts.linear_backward(dy, x, w, r)
     s = off[1] - 1                    # the last row of list 0, beside list 1's first
     dy[off[-1]:] = float("nan")
     dy[s, 5] = float("inf")
     x[entry[s] // m, 7] = float("nan")
-    y, dx, dw = experts.linear(x, w, None, r), *experts.linear_backward(dy, x, w, r)[:2]
+    y, dx, dw, db = experts.linear(x, w, None, r), *experts.linear_backward(dy, x, w, r)
+    assert db[0, 5] == float("inf")
+    db[0, 5] = clean[3][0, 5]
+    assert torch.equal(db, clean[3])
     hit = np.unique(slot[entry[s] // m])
     same = np.setdiff1d(np.arange(off[-1]), hit)
     assert torch.equal(y[same], clean[0][same]) and torch.isnan(y[hit[hit >= 0]]).all()

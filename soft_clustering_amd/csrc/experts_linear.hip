@@ -455,6 +455,72 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_linear_few(const LinArgs a) 
     store4<T, VOUT>((T*)a.c + (int64_t)s * a.ldc, c, a.d_out, v);
 }
 
+constexpr int kBackRows = 8, kBackWaves = 8, kBackOutputs = 512;   // slots, waves, outputs of W in LDS at a time
+
+// dx = dy W on up to 8 rows of a list: a lane owns 16 bytes of columns (VIN) or one, the lanes of a wave that
+// the columns leave over and the waves split the contraction, and the partial sums are added in a
+// fixed order.  The rows of W_k pass once, whole; dy waits in LDS as [output][slot].
+template <typename T, bool VIN>
+__global__ __launch_bounds__(64 * kBackWaves) void k_linear_few_back(const LinArgs a, int lanes_log2) {
+    constexpr int V = VIN ? Vec16<T>::kElems : 1, kAhead = 4;
+    __shared__ __align__(16) float dy[kBackOutputs][kBackRows];
+    __shared__ float part[kBackWaves][64 * V];
+    const int row_block = blockIdx.x / a.col_blocks, lanes = 1 << lanes_log2;
+    const ListRows lr = find_rows(a.offsets, a.K, a.rows, row_block, kBackRows, a.by_slot);
+    if (lr.k < 0) return;
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, subs = 64 >> lanes_log2;
+    const int c = (blockIdx.x % a.col_blocks * lanes + (lane & (lanes - 1))) * V, sub = lane >> lanes_log2;
+    const int n = min(kBackRows, lr.s1 - lr.s0);
+    const T* w = (const T*)a.w + (int64_t)lr.k * a.d_out * a.d_in + (c < a.d_in ? c : 0);
+    float acc[kBackRows][V] = {};
+    for (int o0 = 0; o0 < a.d_out; o0 += kBackOutputs) {
+        const int here = min(kBackOutputs, a.d_out - o0);
+        __syncthreads();   // the last outputs are through
+        for (int i = t; i < kBackOutputs * kBackRows; i += 64 * kBackWaves) {
+            const int r = i / kBackOutputs, o = i % kBackOutputs;
+            dy[o][r] = r < n && o < here ? to_f32(((const T*)a.a)[(int64_t)(lr.s0 + r) * a.lda + o0 + o]) : 0.0f;
+        }
+        __syncthreads();
+        const int stride = kBackWaves * subs;
+        for (int o = wave * subs + sub; o < here; o += kAhead * stride) {
+            float v[kAhead][V];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const T* row = w + (int64_t)(o0 + min(o + u * stride, here - 1)) * a.d_in;
+                if constexpr (VIN) Vec16<T>::unpack(*(const uint4*)row, v[u]);
+                else v[u][0] = to_f32(*row);
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (o + u * stride < here) {
+#pragma unroll
+                    for (int r = 0; r < kBackRows; ++r)
+#pragma unroll
+                        for (int e = 0; e < V; ++e) acc[r][e] = fmaf(dy[o + u * stride][r], v[u][e], acc[r][e]);
+                }
+        }
+    }
+    for (int r = 0; r < n; ++r) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            float sum = 0.0f;   // acc[r][e]
+#pragma unroll
+            for (int q = 0; q < kBackRows; ++q) sum = q == r ? acc[q][e] : sum;
+            for (int m = lanes; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
+            if (sub == 0) part[wave][(lane & (lanes - 1)) * V + e] = sum;
+        }
+        __syncthreads();
+        for (int i = t; i < lanes * V; i += 64 * kBackWaves) {
+            const int to = blockIdx.x % a.col_blocks * lanes * V + i;
+            float sum = 0.0f;
+#pragma unroll
+            for (int q = 0; q < kBackWaves; ++q) sum += part[q][i];
+            if (to < a.d_in) from_f32(sum, (T*)a.c + (int64_t)(lr.s0 + r) * a.ldc + to);
+        }
+        __syncthreads();
+    }
+}
+
 // ---- gradient of the weights
 
 struct GradArgs {
@@ -743,6 +809,19 @@ template <typename T, bool VIN, bool VOUT> gmm_status launch_few(const LinArgs& 
     return launched();
 }
 
+template <typename T, bool VIN> gmm_status launch_few_back(const LinArgs& a, hipStream_t stream) {
+    LinArgs b = a;
+    int grid, lg = 0;
+    const int pieces = VIN ? a.d_in / Vec16<T>::kElems : a.d_in, line = VIN ? 8 : 128 / (int)sizeof(T);
+    while ((1 << lg) < line && (1 << lg) < pieces) ++lg;   // at most a line of W's row a workgroup
+    b.row_blocks = (int)row_blocks(a.rows, a.K, kBackRows, &b.by_slot);
+    b.col_blocks = blocks_of(pieces, 1 << lg);
+    const gmm_status st = grid_of((int64_t)b.row_blocks * b.col_blocks, &grid);
+    if (st != GMM_OK) return st;
+    hipLaunchKernelGGL((k_linear_few_back<T, VIN>), dim3(b.row_blocks * b.col_blocks), dim3(64 * kBackWaves), 0, stream, b, lg);
+    return launched();
+}
+
 // Small: 128 x 128 tiles, several workgroups a compute unit, whose waits hide behind each
 // other.  Large: 256 x 256, half the operand traffic a product, one workgroup a compute unit.
 using Small = Shape<2, 2, 64, 2, 3>;
@@ -758,14 +837,24 @@ bool large_tiles(const LinArgs& a, int kd, int nd) {
     return nd > 128 && tiles * (kd < 512 ? kd : 512) >= 512 * 512;
 }
 
-// Without tiles (k_linear_few) up to four rows a list or 128 rows in all (bf16, us,
-// few / Small: 1 list of 64 rows, 1024 -> 1024: 4.7 / 14.7; 16 lists of 8: 11 / 16, of 32: 22 / 16;
-// 256 lists of 4, 1024 -> 256: 28 / 30, of 16: 50 / 31).
-bool few_rows(const LinArgs& a) { return a.rows <= 4 * (int64_t)a.K || a.rows <= 128; }
+// Without tiles (k_linear_few, k_linear_few_back), where a tile would stand alone and its steps
+// wait for each other (us, few / Small.  Forward, 16-bit: 1 list of 64 rows, 1024 -> 1024: 6 / 14; 16
+// lists of 8: 10 / 17, of 32: 21 / 17; 256 of 4, 128 -> 128: 8.5 / 6.1.  Forward, fp32: 16 of 32, 1024 -> 1024: 37 /
+// 78, of 128: 121 / 77; 1 of 1024: 64 / 78.  dx, 16-bit: 16 of 1: 13 / 17, of 4: 23 / 17; 3 of 1, 25 -> 1557: 19 / 39.
+// dx, fp32: 16 of 8: 29 / 80; 64 of 16, 512 -> 512: 56 / 43; 4 of 100, 77 -> 2000: 29 / 187; 256 of 4,
+// 128 -> 128: 20 / 14).
+template <typename T, bool BACK> bool few_rows(const LinArgs& a) {
+    const int64_t k = a.K;
+    if (!BACK) return sizeof(T) == 2 ? a.rows <= 4 * k || a.rows <= 128 : a.rows <= 32 * k || a.rows <= 512;
+    if (sizeof(T) == 2) return a.rows <= k && a.d_out >= 512;
+    return a.rows <= 512 || (a.rows <= 4 * k && a.d_out >= 512);
+}
 
 template <typename T, bool VIN, bool VOUT, bool BACK> gmm_status launch_linear(const LinArgs& a, hipStream_t stream) {
-    if constexpr (!BACK)
-        if (few_rows(a)) return launch_few<T, VIN, VOUT>(a, stream);
+    if (few_rows<T, BACK>(a)) {
+        if constexpr (BACK) return launch_few_back<T, VIN>(a, stream);
+        else return launch_few<T, VIN, VOUT>(a, stream);
+    }
     if constexpr (VIN && VOUT && sizeof(T) == 2)
         if (large_tiles(a, BACK ? a.d_out : a.d_in, BACK ? a.d_in : a.d_out))
             return launch_shape<T, VIN, VOUT, BACK, Large>(a, stream);

@@ -156,6 +156,9 @@ LINEAR = [   # n, m, k, d_in, d_out, dtype, pad
     (33, 1, 2, 77, 130, "f32", 3), (100, 2, 65, 16, 24, "f16", 0), (129, 1, 1, 128, 128, "bf16", 0),
     (500, 3, 7, 77, 93, "f16", 1), (1000, 2, 16, 64, 64, "f32", 0), (1000, 2, 5, 264, 136, "bf16", 0),
     (2731, 3, 300, 40, 56, "f16", 0), (4000, 1, 2, 31, 257, "bf16", 0), (6000, 2, 3, 136, 72, "f32", 4),
+    (3, 1, 3, 25, 1557, "f32", 0), (2, 8, 17, 72, 1030, "bf16", 0), (5, 2, 40, 264, 1024, "f16", 3),
+    (60, 4, 9, 77, 600, "f32", 0), (150, 2, 90, 200, 640, "f32", 0), (1200, 1, 70, 64, 131, "f32", 1),
+    (900, 3, 6, 131, 128, "bf16", 0), (900, 3, 6, 136, 77, "f16", 0),
 ]
 
 

@@ -6,23 +6,26 @@
 //   dW_k  = sum_s dy[s] x_s^T   contraction over the list's rows; neither is contiguous along it
 //   db_k  = sum_s dy[s]
 //
-// A workgroup computes a tile of 64 x 64 blocks, one a wave, each as 2 x 2 blocks of
-// v_mfma_f32_32x32x16 (16-bit storage) or v_mfma_f32_32x32x2_f32, fp32 accumulators.  Operand
-// tiles go through LDS in 16-byte pieces, 64 or 128 bytes of the contraction a step,
-// two or three steps at a time: the pieces of the next steps are fetched while one is multiplied,
-// straight into LDS (global_load_lds) where rows allow 16-byte pieces, through
-// registers where they do not.  An operand contiguous along the contraction is
-// kept [row][step], its pieces XOR-swizzled by the row, and read a fragment (8 or 4
-// elements) at a time; one that is contiguous along the output is kept
-// [contraction][columns] and read with ds_read_b64_tr_b16 (16-bit) or element by
-// element (fp32).  Pieces beyond a row's end, a list's end or the contraction come
-// from 16 zero bytes, so they add nothing.
+// A workgroup computes a tile of 64 x 64 blocks, one a wave, each as 2 x 2
+// blocks of v_mfma_f32_32x32x16 (16-bit storage) or v_mfma_f32_32x32x2_f32,
+// fp32 accumulators.  Operand tiles go through LDS in 16-byte pieces, 64 or 128
+// bytes of the contraction a step, two or three steps at a time: the pieces of
+// the next steps are fetched while one is multiplied, straight into LDS
+// (global_load_lds) where rows allow 16-byte pieces, through registers where
+// they do not.  An operand contiguous along the contraction is kept [row][step],
+// its pieces XOR-swizzled by the row, and read a fragment (8 or 4 elements) at a
+// time; one that is contiguous along the output is kept [contraction][columns]
+// and read with ds_read_b64_tr_b16 (16-bit) or element by element (fp32).
+// Pieces beyond a row's end, a list's end or the contraction come from 16 zero
+// bytes, so they add nothing.
 //
-// Measured (bf16): 32768 rows in 8 lists, 1024 -> 2048: forward 143 us (960 TFLOP/s), dx 136
-// (1010), dw 173 (795); in 64 lists 201, 187, 269: the weights' 268 MB and their gradient's 537 MB
-// pass the memory too.  Bound there by LDS reads and the barrier of each step; 2e6 rows in 256 lists, 128 -> 128, fp16,
-// 225 us: bound by the memory, where the gathered rows pass twice (a point's two lists
-// lie far apart).  fp32 is bound by its products (a sixteenth of the 16-bit rate) and, on short chunks, by latency.
+// Measured (bf16): 32768 rows in 8 lists, 1024 -> 2048: forward 143 us
+// (960 TFLOP/s), dx 136 (1010), dw 173 (795); in 64 lists 201, 187, 269: the
+// weights' 268 MB and their gradient's 537 MB pass the memory too.  Bound there
+// by LDS reads and the barrier of each step; 2e6 rows in 256 lists, 128 -> 128,
+// fp16, 225 us: bound by the memory, where the gathered rows pass twice (a
+// point's two lists lie far apart).  fp32 is bound by its products (a sixteenth
+// of the 16-bit rate) and, on short chunks, by latency.
 //
 // Workgroup -> rows: find_rows (experts_internal.h); the host never learns the lists' lengths.
 

@@ -3,26 +3,29 @@
 //
 //   out[p, o] = sum_i g_i (sum_j (q_kj - 8) s_k,j/group x[p, j] + b_k),  k = idx[p, i]
 //
-// Bound by the codes' bytes and the latency of the first ones, so each listed component's codes are
-// read once a group of up to 16 points, whatever number of them list it.  A workgroup owns 16 outputs
-// of such a group and every component it lists; its eight waves split the contraction into pieces of
-// 128 to 512 columns and, where there are fewer, the components.  A wave holds its columns of x in
-// registers and streams the
-// components' codes past them, up to eight components in flight: 16 points by 16 outputs on
-// v_mfma_f32_16x16x32, whether they list the component or not (the products are free beside the
-// bytes).  The codes become 16-bit floats by bit operations, exactly; one product chain covers one group
-// of columns, and its fp32 result is scaled, weighted with gamma where the point lists
-// the component, and added in fp32.  The halves of a word of codes are
-// nibbles i and i + 4, so x takes the same order.  fp16: 0x6400 | q is 1024 + q, less 1032.  bf16:
-// 0x4300 | q is 128 + q, and a second product with -136 takes the offset off.  fp32 rows are
+// Bound by the codes' bytes and the latency of the first ones, so each listed
+// component's codes are read once a group of up to 16 points, whatever number
+// of them list it.  A workgroup owns 16 outputs of such a group and every
+// component it lists; its eight waves split the contraction into pieces of 128
+// to 512 columns and, where there are fewer, the components.  A wave holds its
+// columns of x in registers and streams the components' codes past them, up to
+// eight components in flight: 16 points by 16 outputs on v_mfma_f32_16x16x32,
+// whether they list the component or not (the products are free beside the
+// bytes).  The codes become 16-bit floats by bit operations, exactly; one
+// product chain covers one group of columns, and its fp32 result is scaled,
+// weighted with gamma where the point lists the component, and added in fp32.
+// The halves of a word of codes are nibbles i and i + 4, so x takes the same
+// order.  fp16: 0x6400 | q is 1024 + q, less 1032.  bf16: 0x4300 | q is
+// 128 + q, and a second product with -136 takes the offset off.  fp32 rows are
 // split into three bf16 parts, which hold all 24 bits, and meet q - 8 in bf16.
-
 //
-// Measured: one point in two of 16 models 4096 -> 4096 (bf16, groups of 128) 8.4 us, 17 MB of codes; 24
-// points in four of 64 models 1024 -> 2048 (fp16, groups of 64) 33 us.  Lanes that hold different rows
-// of weights load from different lines, 64 cycles an instruction; so codes and x come into LDS row by
-// row, and the scales are staged there for all components of a phase: with loads straight into the
-// operands' registers the batch took 51 us, 20 of them for the scales.
+// Measured: one point in two of 16 models 4096 -> 4096 (bf16, groups of 128)
+// 8.4 us, 17 MB of codes; 24 points in four of 64 models 1024 -> 2048 (fp16,
+// groups of 64) 32 us.  Lanes that hold different rows of weights load from
+// different lines, 64 cycles an instruction; so codes and x come into LDS row
+// by row, and the scales are staged there for all components of a phase: with
+// loads straight into the operands' registers the batch took 51 us, 20 of them
+// for the scales.
 
 #include <type_traits>
 

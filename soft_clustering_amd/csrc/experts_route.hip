@@ -8,12 +8,13 @@
 // its key (one ballot per bit of the key).  Nothing depends on the order of
 // atomics: they only count.
 //
-// A workgroup of eight waves sorts a chunk of up to 8192 (16384) entries, its keys in
-// registers, in LDS first, so that entry[] leaves in runs.  A small assignment is one chunk and one launch;
-// larger ones take three: count per chunk, scan over chunks, place.  1e7 points in two of 256
-// lists: 18 + 6 + 76 us; the two passes over idx and the writes are 320 MB, 63 us at the rate of a copy, and
-// placing waits for its LDS counters group by group.  96 entries: 4.6 us, the latency of a load, two
-// scans and a store.
+// A workgroup of eight waves sorts a chunk of up to 8192 (16384) entries, its
+// keys in registers, in LDS first, so that entry[] leaves in runs.  A small
+// assignment is one chunk and one launch; larger ones take three: count per
+// chunk, scan over chunks, place.  1e7 points in two of 256 lists:
+// 18 + 6 + 76 us; the two passes over idx and the writes are 320 MB, 63 us at
+// the rate of a copy, and placing waits for its LDS counters group by group.
+// 96 entries: 4.6 us, the latency of a load, two scans and a store.
 
 #include "experts_internal.h"
 

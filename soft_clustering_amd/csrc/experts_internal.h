@@ -44,6 +44,19 @@ template <> __device__ __forceinline__ f32x4 mma16<float>(const uint4& a, const 
 
 static __device__ __constant__ uint4 zero_piece = {0, 0, 0, 0};
 
+// 16 bytes of global memory at an alignment.  The address space is named because the compiler loses it where
+// an address comes from a select with zero_piece, and a generic load holds up LDS and the loads behind it.
+typedef uint32_t words4 __attribute__((ext_vector_type(4)));
+template <int ALIGN> struct Words4;
+template <> struct Words4<1> { typedef words4 type __attribute__((aligned(1))); };
+template <> struct Words4<2> { typedef words4 type __attribute__((aligned(2))); };
+template <> struct Words4<4> { typedef words4 type __attribute__((aligned(4))); };
+template <> struct Words4<16> { typedef words4 type __attribute__((aligned(16))); };
+template <int ALIGN> __device__ __forceinline__ uint4 load16(const void* p) {
+    const words4 v = *(const __attribute__((address_space(1))) typename Words4<ALIGN>::type*)p;
+    return make_uint4(v.x, v.y, v.z, v.w);
+}
+
 // The 16 bytes from byte c of a row of `width` >= 16 on, at the alignment given, in two steps so
 // that many loads can be in flight: the load itself (of the row's last 16 bytes where fewer are left, of zeros
 // where there is none), and the bits that lie before c, to be dropped later.
@@ -56,7 +69,7 @@ __device__ __forceinline__ Loose load_loose(const char* row, bool there, int64_t
     there = there && c < width;
     const int64_t from = min(c, width - 16);
     Loose l;
-    __builtin_memcpy(&l.v, __builtin_assume_aligned(there ? row + from : zero, ALIGN), 16);
+    l.v = load16<ALIGN>(there ? row + from : zero);
     l.drop = there ? 8 * (int)(c - from) : 0;
     return l;
 }
@@ -82,14 +95,15 @@ template <typename T> __device__ __forceinline__ uint4 load_narrow(const T* row,
     return __builtin_bit_cast(uint4, t);
 }
 
-// 16 bytes of a row of any width from element c on, at any alignment of the elements; zero beyond it.
-template <typename T>
+// 16 bytes of a row from element c on, at any alignment of the elements; zero beyond it.  NARROW: the row may
+// be of less than 16 bytes.  A kernel of its own, as the compiler waits for a load at the end of the
+// branch it is in: with both forms in one loop each step waited for the memory once per piece.
+template <typename T, bool NARROW>
 __device__ __forceinline__ Loose load_piece(const T* row, bool there, int c, int width, const char* zero) {
     constexpr int S = (int)sizeof(T);
-    if (width * S >= 16) return load_loose<S>((const char*)row, there, (int64_t)c * S, (int64_t)width * S, zero);
-    return Loose{load_narrow(row, there, c, width), 0};
+    if (NARROW && width * S < 16) return Loose{load_narrow(row, there, c, width), 0};
+    return load_loose<S>((const char*)row, there, (int64_t)c * S, (int64_t)width * S, zero);
 }
-
 
 // 16 bytes from each lane's address to LDS bytes lds + 16 lane, asynchronously: the wave that
 // issued it waits with wait_pieces() before the barrier that hands the tile over.  Written as asm

@@ -44,8 +44,9 @@ typedef __attribute__((address_space(3))) char lds_char;
 
 // A workgroup: its waves along the rows and along the columns of its tile, the
 // bytes of the contraction a step takes, the steps in LDS (one multiplied, the others on their way)
-// and the workgroups a compute unit is meant to hold.
-template <int WM_, int WN_, int STEP, int STAGES, int HELD> struct Shape {
+// and the workgroups a compute unit is meant to hold.  NARROW: rows may be of less than 16 bytes.
+template <int WM_, int WN_, int STEP, int STAGES, int HELD, bool NARROW = false> struct Shape {
+    static constexpr bool kNarrow = NARROW;
     static constexpr int WM = WM_, WN = WN_, kStep = STEP, kStages = STAGES, kHeld = HELD;
     static constexpr int kThreads = 64 * WM * WN, kM = 64 * WM, kN = 64 * WN;
     static constexpr int kFrags = kStep / 32;   // fragments of a step
@@ -262,7 +263,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear(const 
                 fetch_piece(whole || k0 + ca < kd ? pa[j] : zero, to + (wave * AJ + j) * 1024);
                 pa[j] += sa[j];
             } else {
-                ra[j] = load_piece<T>((const T*)pa[j], there_a[j], k0 + ca, kd, zero);
+                ra[j] = load_piece<T, S::kNarrow>((const T*)pa[j], there_a[j], k0 + ca, kd, zero);
             }
         }
 #pragma unroll
@@ -271,9 +272,9 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear(const 
                 fetch_piece(whole || k0 + (BACK ? rb[j] : ca) < kd ? pb[j] : zero, to + S::kABytes + (wave * BJ + j) * 1024);
             } else if constexpr (BACK) {
                 const int c = n0 + ((lane % CT::kPieces) ^ CT::swz(rb[j])) * E;
-                rl[j] = load_piece<T>((const T*)pb[j], there_b[j] && k0 + rb[j] < kd, c, nd, zero);
+                rl[j] = load_piece<T, S::kNarrow>((const T*)pb[j], there_b[j] && k0 + rb[j] < kd, c, nd, zero);
             } else {
-                rl[j] = load_piece<T>((const T*)pb[j], there_b[j], k0 + ca, kd, zero);
+                rl[j] = load_piece<T, S::kNarrow>((const T*)pb[j], there_b[j], k0 + ca, kd, zero);
             }
             if (BV || BACK) pb[j] += sb[j];
         }
@@ -407,7 +408,7 @@ constexpr int kFewRows = 16, kFewOutputs = 16, kFewWaves = 4;
 // y = x W^T + b on 16 outputs of up to 16 rows of a list: nothing to share between
 // workgroups, so no LDS tiles.  The waves split the contraction, every lane streams its row of
 // W_k and of x into 16 x 16 products, and the four partial blocks are summed in order.
-template <typename T, bool VIN, bool VOUT>
+template <typename T, bool VIN, bool VOUT, bool NARROW>
 __global__ __launch_bounds__(64 * kFewWaves) void k_linear_few(const LinArgs a) {
     constexpr int E = Vec16<T>::kElems, KS = 4 * E;   // contraction of a product
     constexpr int kAhead = 4;                         // products whose pieces are in flight
@@ -429,8 +430,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_linear_few(const LinArgs a) 
     const int mine = (lane >> 4) * E;
     const char* zero = zero_address();
     auto piece = [&](const T* p, bool there, int k) {
-        if constexpr (VIN) return Loose{*(const uint4*)(there && k < a.d_in ? (const char*)(p + k) : zero), 0};
-        else return load_piece<T>(p, there, k, a.d_in, zero);
+        if constexpr (VIN) return Loose{load16<16>(there && k < a.d_in ? (const char*)(p + k) : zero), 0};
+        else return load_piece<T, NARROW>(p, there, k, a.d_in, zero);
     };
     for (int k0 = wave * KS; k0 < a.d_in; k0 += kAhead * kFewWaves * KS) {
         Loose fw[kAhead], fx[kAhead];
@@ -619,13 +620,13 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void k_linear_dw(con
             const bool there = from >= 0 && cx[j] < i1;
             const char* row = (const char*)((const T*)a.x + (int64_t)from * a.ldx);
             if constexpr (VIN) fetch_piece(there ? row + cx[j] * (int)sizeof(T) : zero, to + (wave * XJ + j) * 1024);
-            else rx[j] = load_piece<T>((const T*)row, there, cx[j], a.d_in, zero);
+            else rx[j] = load_piece<T, S::kNarrow>((const T*)row, there, cx[j], a.d_in, zero);
         }
 #pragma unroll
         for (int j = 0; j < YJ; ++j) {
             const bool there = whole || s0 - lr.s0 + rowy[j] < s1;
             if constexpr (VOUT) fetch_piece(there ? py[j] : zero, to + S::kABytes + (wave * YJ + j) * 1024);
-            else ry[j] = load_piece<T>((const T*)py[j], there, cy[j], a.d_out, zero);
+            else ry[j] = load_piece<T, S::kNarrow>((const T*)py[j], there, cy[j], a.d_out, zero);
             py[j] += sy[j];
         }
     };
@@ -801,14 +802,14 @@ gmm_status launch_shape(const LinArgs& a, hipStream_t stream) {
     return launched();
 }
 
-template <typename T, bool VIN, bool VOUT> gmm_status launch_few(const LinArgs& a, hipStream_t stream) {
+template <typename T, bool VIN, bool VOUT, bool NARROW = false> gmm_status launch_few(const LinArgs& a, hipStream_t stream) {
     LinArgs b = a;
     int grid;
     b.row_blocks = (int)row_blocks(a.rows, a.K, kFewRows, &b.by_slot);
     b.col_blocks = blocks_of(a.d_out, kFewOutputs);
     const gmm_status st = grid_of((int64_t)b.row_blocks * b.col_blocks, &grid);
     if (st != GMM_OK) return st;
-    hipLaunchKernelGGL((k_linear_few<T, VIN, VOUT>), dim3(b.row_blocks * b.col_blocks), dim3(64 * kFewWaves), 0, stream, b);
+    hipLaunchKernelGGL((k_linear_few<T, VIN, VOUT, NARROW>), dim3(b.row_blocks * b.col_blocks), dim3(64 * kFewWaves), 0, stream, b);
     return launched();
 }
 
@@ -828,6 +829,7 @@ template <typename T, bool VIN> gmm_status launch_few_back(const LinArgs& a, hip
 // Small: 128 x 128 tiles, several workgroups a compute unit, whose waits hide behind each
 // other.  Large: 256 x 256, half the operand traffic a product, one workgroup a compute unit.
 using Small = Shape<2, 2, 64, 2, 3>;
+using Narrow = Shape<2, 2, 64, 2, 3, true>;
 using Large = Shape<4, 4, 128, 2, 1>;
 using LargeGrad = Shape<4, 4, 64, 3, 1>;
 
@@ -853,11 +855,18 @@ template <typename T, bool BACK> bool few_rows(const LinArgs& a) {
     return a.rows <= 512 || (a.rows <= 4 * k && a.d_out >= 512);
 }
 
+template <typename T> bool narrow_rows(int width) { return width * (int)sizeof(T) < 16; }
+
 template <typename T, bool VIN, bool VOUT, bool BACK> gmm_status launch_linear(const LinArgs& a, hipStream_t stream) {
+    const bool narrow = narrow_rows<T>(a.d_in) || (BACK && narrow_rows<T>(a.d_out));   // among the operands
     if (few_rows<T, BACK>(a)) {
         if constexpr (BACK) return launch_few_back<T, VIN>(a, stream);
-        else return launch_few<T, VIN, VOUT>(a, stream);
+        if constexpr (!BACK && !VIN)
+            if (narrow) return launch_few<T, VIN, VOUT, true>(a, stream);
+        if constexpr (!BACK) return launch_few<T, VIN, VOUT>(a, stream);
     }
+    if constexpr (!VIN || (BACK && !VOUT))
+        if (narrow) return launch_shape<T, VIN, VOUT, BACK, Narrow>(a, stream);
     if constexpr (VIN && VOUT && sizeof(T) == 2)
         if (large_tiles(a, BACK ? a.d_out : a.d_in, BACK ? a.d_in : a.d_out))
             return launch_shape<T, VIN, VOUT, BACK, Large>(a, stream);
@@ -905,7 +914,9 @@ template <typename T, bool VEC> struct GradShape {
 
 template <typename T, bool VIN, bool VOUT> gmm_status launch_dw(const GradArgs& a, hipStream_t stream) {
     gmm_status st;
+    using N = typename std::conditional<VIN && VOUT, Small, Narrow>::type;
     if (VIN && VOUT && sizeof(T) == 2 && large_grad(a)) st = launch_dw_shape<T, VIN, VOUT, typename GradShape<T, VIN && VOUT>::L>(a, stream);
+    else if (narrow_rows<T>(a.d_in) || narrow_rows<T>(a.d_out)) st = launch_dw_shape<T, VIN, VOUT, N>(a, stream);
     else st = launch_dw_shape<T, VIN, VOUT, Small>(a, stream);
     if (st != GMM_OK) return st;
     const int64_t wide = (int64_t)a.d_out * a.d_in;

@@ -159,6 +159,8 @@ LINEAR = [   # n, m, k, d_in, d_out, dtype, pad
     (3, 1, 3, 25, 1557, "f32", 0), (2, 8, 17, 72, 1030, "bf16", 0), (5, 2, 40, 264, 1024, "f16", 3),
     (60, 4, 9, 77, 600, "f32", 0), (150, 2, 90, 200, 640, "f32", 0), (1200, 1, 70, 64, 131, "f32", 1),
     (900, 3, 6, 131, 128, "bf16", 0), (900, 3, 6, 136, 77, "f16", 0),
+    (700, 2, 3, 3, 130, "f32", 0), (700, 2, 3, 130, 2, "f32", 1), (900, 1, 2, 5, 7, "bf16", 0),
+    (900, 3, 4, 200, 3, "f16", 0), (4, 2, 3, 3, 50, "f16", 5), (10, 2, 3, 2, 33, "f32", 0),
 ]
 
 

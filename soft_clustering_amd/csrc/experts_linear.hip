@@ -846,8 +846,8 @@ bool large_tiles(const LinArgs& a, int kd, int nd) {
 // Without tiles (k_linear_few, k_linear_few_back), where a tile would stand alone and its steps
 // wait for each other (us, few / Small.  Forward, 16-bit: 1 list of 64 rows, 1024 -> 1024: 6 / 14; 16
 // lists of 8: 10 / 17, of 32: 21 / 17; 256 of 4, 128 -> 128: 8.5 / 6.1.  Forward, fp32: 16 of 32, 1024 -> 1024: 37 /
-// 78, of 128: 121 / 77; 1 of 1024: 64 / 78.  dx, 16-bit: 16 of 1: 13 / 17, of 4: 23 / 17; 3 of 1, 25 -> 1557: 19 / 39.
-// dx, fp32: 16 of 8: 29 / 80; 64 of 16, 512 -> 512: 56 / 43; 4 of 100, 77 -> 2000: 29 / 187; 256 of 4,
+// 78, of 128: 121 / 77; 1 of 1024: 64 / 78.  dx, 16-bit: 16 of 1: 13 / 17, of 4: 23 / 17; 3 of 1, 25 -> 1557: 18 / 29.
+// dx, fp32: 16 of 8: 29 / 80; 64 of 16, 512 -> 512: 56 / 43; 4 of 100, 77 -> 2000: 28 / 166; 256 of 4,
 // 128 -> 128: 20 / 14).
 template <typename T, bool BACK> bool few_rows(const LinArgs& a) {
     const int64_t k = a.K;
